@@ -54,7 +54,8 @@ typedef enum {
     W4A8_ERR_CUDA = 4,            /* a CUDA runtime call or kernel launch failed */
     W4A8_ERR_TIMEOUT = 5,         /* a bounded device-side wait ran out (see w4a8_get_device_status) */
     W4A8_ERR_UNSUPPORTED = 6,     /* the current device is not sm_103, or the shape exceeds a kernel limit */
-    W4A8_ERR_WORKSPACE = 7        /* the workspace passed is NULL or smaller than w4a8_workspace_bytes */
+    W4A8_ERR_WORKSPACE = 7,       /* the workspace passed is NULL or smaller than w4a8_workspace_bytes */
+    W4A8_ERR_PAGE = 8             /* device status: a page table, start or slot named no place of the KV cache */
 } w4a8_status;
 
 /* Kernel choice.  The pages switch kernels with the inference phase; here
@@ -234,6 +235,113 @@ size_t w4a8_decode_attention_workspace_bytes(int B, int Hq, int Hkv, int D, int 
 w4a8_status w4a8_decode_attention(const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache,
                                   const int32_t *lens, int B, int Hq, int Hkv, int D, int Lmax, uint16_t *out,
                                   void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Attention of whole prompts (prefill, the compute-bound phase of the pages'
+ * section cited above): B sequences of different lengths, packed.
+ *   q        rows of [Hq][D] fp16, ld_q elements between tokens; sequence b's
+ *            query tokens are rows cu_q[b] .. cu_q[b+1]-1 of Tq
+ *   k, v     rows of [Hkv][D] fp16, ld_k and ld_v elements between tokens;
+ *            its keys and values are rows cu_k[b] .. cu_k[b+1]-1 of Tk.  q, k
+ *            and v may be parts of one fused projection's output
+ *   cu_q, cu_k  [B+1] int32, device, ascending from 0 (clamped into the rows
+ *            there are; 4-byte aligned)
+ *   out      [Tq][Hq][D] fp16, dense
+ *   out[i][h] = sum_j softmax_j(scale q_i.k_j) v_j over the sequence's keys,
+ *            KV head h / (Hq/Hkv), fp32 scores, sums and accumulators, the
+ *            weights rounded to fp16 before the product with v.
+ * A sequence's queries are its last tokens: with nq queries and nk keys, query
+ * i is at place i + nk - nq, and where `causal` is not 0 it sees the keys up
+ * to that place.  A query that sees no key gets zeros; rows of q that belong
+ * to no sequence leave out as it was.  Neighbours in the packing never reach
+ * a sequence's results, whatever they hold.
+ * Requires D in {64, 128, 256}, Hq % Hkv == 0, Hq/Hkv <= 128, strides that are
+ * multiples of 8 and cover a token, scale finite and > 0; Tq and Tk may be 0
+ * (nothing runs when Tq is).  Needs no workspace. */
+w4a8_status w4a8_prompt_attention(const uint16_t *q, const uint16_t *k, const uint16_t *v,
+                                  long long ld_q, long long ld_k, long long ld_v,
+                                  const int32_t *cu_q, const int32_t *cu_k, int B, int Tq, int Tk,
+                                  int Hq, int Hkv, int D, int causal, float scale, uint16_t *out, cudaStream_t stream);
+
+/* A KV cache held in 8 bits, in pages.  The pages' decode protocol keeps the
+ * cache in fp16 (section cited above); codes with a scale per 16 tokens of a
+ * head halve the bytes that a decode step reads.
+ *   k_codes, v_codes  [pages][heads][page_tokens][dim] int8 in [-127, 127]
+ *   k_scale, v_scale  [pages][heads][page_tokens/16] fp32, >= 0
+ * page_tokens is 16, 32, 64 or 128, dim 64, 128 or 256.  Value = code * scale.
+ * A page table is int32 [B][max_pages], device: token p of sequence b is token
+ * p % page_tokens of page table[b][p / page_tokens].  Index arrays (tables,
+ * lengths, places) need 4-byte alignment, all other pointers 16.  An index
+ * array that names no place of the cache makes the kernels skip that access
+ * (as the calls below say) and sets W4A8_ERR_PAGE in the device status. */
+typedef struct {
+    int8_t *k_codes;
+    float *k_scale;
+    int8_t *v_codes;
+    float *v_scale;
+    int pages, heads, page_tokens, dim;
+} w4a8_kv8;
+
+/* Writes new tokens: sequence b holds start[b] tokens and gets the rows cu[b]
+ * .. cu[b+1]-1 of k and v (fp16 rows of [heads][dim], ld_k and ld_v elements
+ * apart, `total` rows in all) behind them.  Per 16 tokens of a head (fp32):
+ *   s = max(s_old, amax of the block's new values / 127); new codes are
+ *   clamp(round_half_even(x / s), -127, 127), all 0 where s is 0; where s >
+ *   s_old the block's earlier codes become round_half_even(code * (s_old / s)).
+ * s_old counts only where the block holds earlier tokens of the sequence, so
+ * what is behind a sequence's end never matters.  Tokens whose page the table
+ * does not name are dropped.  Requires k and v finite, and pages written by
+ * one sequence only (w4a8_kv8_fork copies the page that two would write). */
+w4a8_status w4a8_kv8_append(const w4a8_kv8 *cache, const uint16_t *k, const uint16_t *v, long long ld_k, long long ld_v,
+                            const int32_t *table, const int32_t *start, const int32_t *cu, int B, int max_pages,
+                            int total, cudaStream_t stream);
+
+/* Reads tokens back as fp16(code * scale): sequence b's first cu[b+1] - cu[b]
+ * tokens into the rows from cu[b] of k_out and v_out ([total][heads][dim],
+ * dense), as w4a8_prompt_attention takes them (a prompt that goes on behind a
+ * prefix in the cache).  Tokens on no page read as zeros. */
+w4a8_status w4a8_kv8_read(const w4a8_kv8 *cache, const int32_t *table, const int32_t *cu, int B, int max_pages,
+                          int total, uint16_t *k_out, uint16_t *v_out, cudaStream_t stream);
+
+/* Decode attention over the 8-bit cache, one new token per sequence:
+ *   out[b][h] = sum_t softmax_t(scale q[b][h].k_t) v_t, t < lens[b] (clamped
+ *   to [0, max_pages page_tokens]; zeros for a length of 0), KV head
+ *   h / (Hq/heads), fp32 scores, sums and accumulators, the weights rounded to
+ *   fp16 before the product with v's codes.  q, out [B][Hq][dim] fp16.
+ * Tokens on no page are left out.  Requires Hq % heads == 0, Hq/heads <= 16,
+ * B <= 65535, max_pages * page_tokens < 2^31, scale finite and > 0, and a
+ * workspace of w4a8_decode_attention_kv8_workspace_bytes (0 for an invalid
+ * shape; it does not grow with the length). */
+size_t w4a8_decode_attention_kv8_workspace_bytes(int B, int Hq, int Hkv, int D, int page_tokens, int max_pages);
+w4a8_status w4a8_decode_attention_kv8(const uint16_t *q, const w4a8_kv8 *cache, const int32_t *table,
+                                      const int32_t *lens, int B, int Hq, int max_pages, float scale, uint16_t *out,
+                                      void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* The pages of a cache follow from a table of S rows and the rows' lengths: a
+ * page is held when a row names it among its first ceil(len / page_tokens)
+ * entries.  A sequence is freed by setting its length to 0.
+ *
+ * free_pages: the pages that no row holds, ascending, in ids [pages] (-1 behind
+ * the last), their number in count[1]. */
+w4a8_status w4a8_kv8_free_pages(const int32_t *table, const int32_t *lens, int S, int max_pages, int page_tokens,
+                                int pages, int32_t *ids, int32_t *count, cudaStream_t stream);
+
+/* fork: row dst[i] becomes a copy of row src[i] (its length too; entries behind
+ * it -1) that shares its full pages; the last page, where it is not full, is
+ * copied into page fresh[i], which must be free.  No dst may be a src or come
+ * twice.  A fork that needs a place that is not there is not made. */
+w4a8_status w4a8_kv8_fork(const w4a8_kv8 *cache, int32_t *table, int32_t *lens, const int32_t *src, const int32_t *dst,
+                          const int32_t *fresh, int n, int S, int max_pages, cudaStream_t stream);
+
+/* compact: moves the n held pages into pages 0 .. n-1: the held pages from n
+ * on, ascending, go to the free pages below n, ascending (each page's source
+ * stays as it was).  table_out (not table itself) gets the rows with the moved
+ * pages' new numbers, -1 behind a row's held entries; count[0] = n.  Needs a
+ * workspace of w4a8_kv8_compact_workspace_bytes.  free_pages and compact take
+ * up to 12582912 pages (W4A8_ERR_UNSUPPORTED above). */
+size_t w4a8_kv8_compact_workspace_bytes(int pages);
+w4a8_status w4a8_kv8_compact(const w4a8_kv8 *cache, const int32_t *table, const int32_t *lens, int S, int max_pages,
+                             int32_t *table_out, int32_t *count, void *workspace, size_t workspace_bytes,
+                             cudaStream_t stream);
 
 /* Debug: the activation quantiser alone, through the same device routine
  * the linear kernels use.  codes [M][K] int8 and sx [M][K/32] fp32, device. */

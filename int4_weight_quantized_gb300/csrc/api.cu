@@ -15,6 +15,8 @@
 #include "kernels.h"
 #include "sync.cuh"
 
+using namespace w4a8_host;
+
 namespace {
 
 // Sticky device status: W4A8_OK or the first error a kernel recorded.
@@ -49,6 +51,33 @@ w4a8_status check_device() {
         return W4A8_ERR_CUDA;
     }
     return device_cc(dev) == 103 ? W4A8_OK : W4A8_ERR_UNSUPPORTED;
+}
+
+bool aligned4(const void *p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+bool head_dim_ok(int D) { return D == 64 || D == 128 || D == 256; }
+
+bool page_tokens_ok(int T) { return T == 16 || T == 32 || T == 64 || T == 128; }
+
+bool scale_ok(float s) { return s > 0.0f && s <= 3.0e38f; }
+
+// Rows of heads x D with `ld` elements between tokens: TMA and the 16-byte
+// loads want multiples of 16 bytes, and a tensor map's strides end at 2^40.
+bool stride_ok(long long ld, int heads, int D) {
+    return ld % 8 == 0 && ld >= (long long)heads * D && ld < (1LL << 39);
+}
+
+bool table_ok(int B, int max_pages, int T) {
+    return B >= 1 && B <= 65535 && max_pages >= 1 && (long long)max_pages * T <= 0x7fffffffLL;
+}
+
+w4a8_status check_cache(const w4a8_kv8 *c, Kv8Cache *out) {
+    if (!c || c->pages < 1 || c->heads < 1 || c->heads > 65535 || !page_tokens_ok(c->page_tokens) || !head_dim_ok(c->dim))
+        return W4A8_ERR_INVALID_VALUE;
+    if (!aligned16(c->k_codes) || !aligned16(c->v_codes) || !aligned16(c->k_scale) || !aligned16(c->v_scale))
+        return W4A8_ERR_MISALIGNED;
+    *out = {c->k_codes, c->v_codes, c->k_scale, c->v_scale, c->pages, c->heads, c->page_tokens, c->dim};
+    return W4A8_OK;
 }
 
 bool shape_ok(int M, int N, int K) { return M >= 1 && N >= 1 && K >= 32 && K % 32 == 0; }
@@ -111,6 +140,7 @@ const char *w4a8_status_string(w4a8_status s) {
         case W4A8_ERR_TIMEOUT: return "bounded device wait timed out";
         case W4A8_ERR_UNSUPPORTED: return "unsupported device or shape";
         case W4A8_ERR_WORKSPACE: return "workspace missing or too small";
+        case W4A8_ERR_PAGE: return "an index named no place of the KV cache";
     }
     return "unknown status";
 }
@@ -281,6 +311,127 @@ w4a8_status w4a8_decode_attention(const uint16_t *q, const uint16_t *k_cache, co
     if (st != W4A8_OK) return st;
     cudaGetLastError();
     return launch_attention(q, k_cache, v_cache, lens, B, Hq, Hkv, D, Lmax, out, workspace, workspace_bytes, stream);
+}
+
+w4a8_status w4a8_prompt_attention(const uint16_t *q, const uint16_t *k, const uint16_t *v, long long ld_q,
+                                  long long ld_k, long long ld_v, const int32_t *cu_q, const int32_t *cu_k, int B, int Tq,
+                                  int Tk, int Hq, int Hkv, int D, int causal, float scale, uint16_t *out,
+                                  cudaStream_t stream) {
+    if (B < 1 || B > 65535 || Tq < 0 || Tk < 0 || Hkv < 1 || Hq < 1 || Hq > 65535 || Hq % Hkv != 0 || Hq / Hkv > 128 ||
+        !head_dim_ok(D) || !scale_ok(scale))
+        return W4A8_ERR_INVALID_VALUE;
+    if (!stride_ok(ld_q, Hq, D) || !stride_ok(ld_k, Hkv, D) || !stride_ok(ld_v, Hkv, D)) return W4A8_ERR_INVALID_VALUE;
+    // one CTA per KV head and item: at least one token each
+    if (((long long)Tq + B) * Hkv > 0x7fffffffLL) return W4A8_ERR_INVALID_VALUE;
+    if (!aligned4(cu_q) || !aligned4(cu_k)) return W4A8_ERR_MISALIGNED;
+    if (Tq > 0 && (!aligned16(q) || !aligned16(out))) return W4A8_ERR_MISALIGNED;
+    if (Tk > 0 && (!aligned16(k) || !aligned16(v))) return W4A8_ERR_MISALIGNED;
+    w4a8_status st = check_device();
+    if (st != W4A8_OK || Tq == 0) return st;
+    cudaGetLastError();
+    const PromptShape s = {B, Tq, Tk, Hq, Hkv, D, ld_q, ld_k, ld_v};
+    return launch_prompt_attention(q, k, v, cu_q, cu_k, s, causal != 0, scale, out, stream);
+}
+
+w4a8_status w4a8_kv8_append(const w4a8_kv8 *cache, const uint16_t *k, const uint16_t *v, long long ld_k, long long ld_v,
+                            const int32_t *table, const int32_t *start, const int32_t *cu, int B, int max_pages,
+                            int total, cudaStream_t stream) {
+    Kv8Cache c;
+    w4a8_status st = check_cache(cache, &c);
+    if (st != W4A8_OK) return st;
+    if (!table_ok(B, max_pages, c.T) || total < 0 || !stride_ok(ld_k, c.Hkv, c.D) || !stride_ok(ld_v, c.Hkv, c.D))
+        return W4A8_ERR_INVALID_VALUE;
+    if (!aligned4(table) || !aligned4(start) || !aligned4(cu)) return W4A8_ERR_MISALIGNED;
+    if (total > 0 && (!aligned16(k) || !aligned16(v))) return W4A8_ERR_MISALIGNED;
+    st = check_device();
+    if (st != W4A8_OK || total == 0) return st;
+    cudaGetLastError();
+    return launch_kv8_append(k, v, ld_k, ld_v, c, table, start, cu, B, max_pages, total, stream);
+}
+
+w4a8_status w4a8_kv8_read(const w4a8_kv8 *cache, const int32_t *table, const int32_t *cu, int B, int max_pages,
+                          int total, uint16_t *k_out, uint16_t *v_out, cudaStream_t stream) {
+    Kv8Cache c;
+    w4a8_status st = check_cache(cache, &c);
+    if (st != W4A8_OK) return st;
+    if (!table_ok(B, max_pages, c.T) || total < 0) return W4A8_ERR_INVALID_VALUE;
+    if (!aligned4(table) || !aligned4(cu)) return W4A8_ERR_MISALIGNED;
+    if (total > 0 && (!aligned16(k_out) || !aligned16(v_out))) return W4A8_ERR_MISALIGNED;
+    st = check_device();
+    if (st != W4A8_OK || total == 0) return st;
+    cudaGetLastError();
+    return launch_kv8_read(c, table, cu, B, max_pages, total, k_out, v_out, stream);
+}
+
+static bool decode_kv8_shape_ok(int B, int Hq, int Hkv, int D, int T, int max_pages) {
+    return head_dim_ok(D) && page_tokens_ok(T) && table_ok(B, max_pages, T) && Hkv >= 1 && Hq >= 1 && Hq <= 65535 &&
+           Hq % Hkv == 0 && Hq / Hkv <= 16;
+}
+
+size_t w4a8_decode_attention_kv8_workspace_bytes(int B, int Hq, int Hkv, int D, int page_tokens, int max_pages) {
+    if (!decode_kv8_shape_ok(B, Hq, Hkv, D, page_tokens, max_pages)) return 0;
+    return kv8_decode_workspace_bytes(B, Hq, Hkv, D, page_tokens, max_pages);
+}
+
+w4a8_status w4a8_decode_attention_kv8(const uint16_t *q, const w4a8_kv8 *cache, const int32_t *table,
+                                      const int32_t *lens, int B, int Hq, int max_pages, float scale, uint16_t *out,
+                                      void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+    Kv8Cache c;
+    w4a8_status st = check_cache(cache, &c);
+    if (st != W4A8_OK) return st;
+    if (!decode_kv8_shape_ok(B, Hq, c.Hkv, c.D, c.T, max_pages) || !scale_ok(scale)) return W4A8_ERR_INVALID_VALUE;
+    if (!aligned16(q) || !aligned16(out) || !aligned4(table) || !aligned4(lens)) return W4A8_ERR_MISALIGNED;
+    if (!aligned16(workspace) || workspace_bytes < kv8_decode_workspace_bytes(B, Hq, c.Hkv, c.D, c.T, max_pages))
+        return W4A8_ERR_WORKSPACE;
+    st = check_device();
+    if (st != W4A8_OK) return st;
+    cudaGetLastError();
+    return launch_kv8_decode(q, c, table, lens, B, Hq, max_pages, scale, out, workspace, stream);
+}
+
+w4a8_status w4a8_kv8_free_pages(const int32_t *table, const int32_t *lens, int S, int max_pages, int page_tokens,
+                                int pages, int32_t *ids, int32_t *count, cudaStream_t stream) {
+    if (!page_tokens_ok(page_tokens) || !table_ok(S, max_pages, page_tokens) || pages < 1) return W4A8_ERR_INVALID_VALUE;
+    if (!aligned4(table) || !aligned4(lens) || !aligned4(ids) || !aligned4(count)) return W4A8_ERR_MISALIGNED;
+    if (!kv8_pages_supported(pages)) return W4A8_ERR_UNSUPPORTED;
+    w4a8_status st = check_device();
+    if (st != W4A8_OK) return st;
+    cudaGetLastError();
+    return launch_kv8_free_pages(table, lens, S, max_pages, page_tokens, pages, ids, count, stream);
+}
+
+w4a8_status w4a8_kv8_fork(const w4a8_kv8 *cache, int32_t *table, int32_t *lens, const int32_t *src, const int32_t *dst,
+                          const int32_t *fresh, int n, int S, int max_pages, cudaStream_t stream) {
+    Kv8Cache c;
+    w4a8_status st = check_cache(cache, &c);
+    if (st != W4A8_OK) return st;
+    if (!table_ok(S, max_pages, c.T) || n < 0 || n > 65535) return W4A8_ERR_INVALID_VALUE;
+    if (!aligned4(table) || !aligned4(lens)) return W4A8_ERR_MISALIGNED;
+    if (n > 0 && (!aligned4(src) || !aligned4(dst) || !aligned4(fresh))) return W4A8_ERR_MISALIGNED;
+    st = check_device();
+    if (st != W4A8_OK || n == 0) return st;
+    cudaGetLastError();
+    return launch_kv8_fork(c, table, lens, src, dst, fresh, n, S, max_pages, stream);
+}
+
+size_t w4a8_kv8_compact_workspace_bytes(int pages) {
+    return pages >= 1 && kv8_pages_supported(pages) ? kv8_compact_workspace_bytes(pages) : 0;
+}
+
+w4a8_status w4a8_kv8_compact(const w4a8_kv8 *cache, const int32_t *table, const int32_t *lens, int S, int max_pages,
+                             int32_t *table_out, int32_t *count, void *workspace, size_t workspace_bytes,
+                             cudaStream_t stream) {
+    Kv8Cache c;
+    w4a8_status st = check_cache(cache, &c);
+    if (st != W4A8_OK) return st;
+    if (!table_ok(S, max_pages, c.T) || table_out == table) return W4A8_ERR_INVALID_VALUE;
+    if (!aligned4(table) || !aligned4(lens) || !aligned4(table_out) || !aligned4(count)) return W4A8_ERR_MISALIGNED;
+    if (!kv8_pages_supported(c.P)) return W4A8_ERR_UNSUPPORTED;
+    if (!aligned16(workspace) || workspace_bytes < kv8_compact_workspace_bytes(c.P)) return W4A8_ERR_WORKSPACE;
+    st = check_device();
+    if (st != W4A8_OK) return st;
+    cudaGetLastError();
+    return launch_kv8_compact(c, table, lens, S, max_pages, table_out, count, workspace, stream);
 }
 
 w4a8_status w4a8_debug_quantize_act(const uint16_t *x, int M, int K, int8_t *codes, float *sx,

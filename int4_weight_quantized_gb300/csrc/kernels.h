@@ -105,6 +105,43 @@ w4a8_status launch_attention(const uint16_t *q, const uint16_t *k, const uint16_
                              int Hkv, int D, int Lmax, uint16_t *out, void *workspace, size_t workspace_bytes,
                              cudaStream_t stream);
 
+// Attention of packed prompts on the tensor cores (prompt_attention.cu): Tq
+// query and Tk key rows in all, ld_* elements between tokens.
+struct PromptShape {
+    int B, Tq, Tk, Hq, Hkv, D;
+    long long ld_q, ld_k, ld_v;
+};
+w4a8_status launch_prompt_attention(const uint16_t *q, const uint16_t *k, const uint16_t *v, const int32_t *cu_q,
+                                    const int32_t *cu_k, const PromptShape &s, int causal, float scale, uint16_t *out,
+                                    cudaStream_t stream);
+
+// 8-bit paged KV cache: codes [P][Hkv][T][D], scales [P][Hkv][T/16].
+struct Kv8Cache {
+    int8_t *k_codes, *v_codes;
+    float *k_scale, *v_scale;
+    int P, Hkv, T, D;
+};
+// Writing `rows` packed new tokens, reading packed tokens back (kv8_cache.cu);
+// table int32 [B][maxp].
+w4a8_status launch_kv8_append(const uint16_t *k, const uint16_t *v, long long ld_k, long long ld_v, const Kv8Cache &c,
+                              const int32_t *table, const int32_t *start, const int32_t *cu, int B, int maxp, int rows,
+                              cudaStream_t stream);
+w4a8_status launch_kv8_read(const Kv8Cache &c, const int32_t *table, const int32_t *cu, int B, int maxp, int rows,
+                            uint16_t *k, uint16_t *v, cudaStream_t stream);
+// Decode attention over it (kv8_attention.cu).
+size_t kv8_decode_workspace_bytes(int B, int Hq, int Hkv, int D, int T, int maxp);
+w4a8_status launch_kv8_decode(const uint16_t *q, const Kv8Cache &c, const int32_t *table, const int32_t *lens, int B,
+                              int Hq, int maxp, float scale, uint16_t *out, void *workspace, cudaStream_t stream);
+// Its pages (kv8_pages.cu).
+bool kv8_pages_supported(int P);
+size_t kv8_compact_workspace_bytes(int P);
+w4a8_status launch_kv8_free_pages(const int32_t *table, const int32_t *lens, int S, int maxp, int T, int P, int32_t *ids,
+                                  int32_t *count, cudaStream_t stream);
+w4a8_status launch_kv8_compact(const Kv8Cache &c, const int32_t *table, const int32_t *lens, int S, int maxp,
+                               int32_t *table_out, int32_t *count, void *workspace, cudaStream_t stream);
+w4a8_status launch_kv8_fork(const Kv8Cache &c, int32_t *table, int32_t *lens, const int32_t *src, const int32_t *dst,
+                            const int32_t *fresh, int n, int S, int maxp, cudaStream_t stream);
+
 // The plain linear on the automatically chosen path (api.cu), and its
 // workspace size; used by the gated pair's unfused route.
 size_t linear_workspace_bytes(int M, int N, int K);

@@ -1,0 +1,49 @@
+// kv8_index.h -- index arithmetic of the 8-bit paged KV cache and of packed
+// sequences, as plain functions that the kernels and the CPU tests share.
+//
+// Cache layout (this library's): codes int8 [P][Hkv][T][D], scales fp32
+// [P][Hkv][T/16]: a page holds T tokens (a multiple of 16) of every KV head,
+// and 16 consecutive tokens of a head share a scale.  Token p of a sequence
+// is token p % T of page table[p / T].
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+#ifdef __CUDACC__
+#define KV8_FN __host__ __device__ __forceinline__
+#else
+#define KV8_FN static inline
+#endif
+
+namespace kv8 {
+
+constexpr int kBlockTokens = 16;     // tokens that share a scale
+
+// First code of token `tok` of a page's head, and the scale of its block
+// (64-bit: a cache of more than 2^31 codes is ordinary).
+KV8_FN size_t code_offset(int page, int Hkv, int head, int T, int tok, int D) {
+    return (((size_t)page * Hkv + head) * T + tok) * (size_t)D;
+}
+KV8_FN size_t scale_offset(int page, int Hkv, int head, int T, int tok) {
+    return ((size_t)page * Hkv + head) * (size_t)(T / kBlockTokens) + tok / kBlockTokens;
+}
+
+// Packed sequences: sequence b has rows cu[b] .. cu[b+1] - 1.  Work items of
+// `unit` rows are numbered without a pass over all lengths: sequence b's
+// items begin at cu[b] / unit + slack * b.  That leaves it at least
+// floor(n / unit) + slack numbers for its n rows: enough for ceil(n / unit)
+// items with slack 1, and for the 16-token blocks that n rows touch from any
+// starting place with slack 2.  The numbers that are left over are idle.
+KV8_FN int item_base(int cu_b, int unit, int slack, int b) { return cu_b / unit + slack * b; }
+KV8_FN int item_count(int total_rows, int unit, int slack, int B) { return total_rows / unit + slack * B; }
+
+// Blocks of 16 tokens that rows start .. start + n - 1 touch (n >= 1).
+KV8_FN int touched_blocks(int start, int n) { return (start % kBlockTokens + n - 1) / kBlockTokens + 1; }
+
+// U units split over C workers in order: worker c takes units
+// [first_unit(c), first_unit(c + 1)), sizes differing by at most one.
+KV8_FN long long first_unit(long long c, long long U, long long C) { return c * U / C; }
+KV8_FN int worker_of_unit(long long u, long long U, long long C) { return (int)(((u + 1) * C - 1) / U); }
+
+}  // namespace kv8

@@ -1,0 +1,12 @@
+// C entry points to the index arithmetic that the kernels use, for the CPU tests.
+#include "kv8_index.h"
+
+extern "C" {
+size_t code_offset(int page, int Hkv, int head, int T, int tok, int D) { return kv8::code_offset(page, Hkv, head, T, tok, D); }
+size_t scale_offset(int page, int Hkv, int head, int T, int tok) { return kv8::scale_offset(page, Hkv, head, T, tok); }
+int item_base(int cu_b, int unit, int slack, int b) { return kv8::item_base(cu_b, unit, slack, b); }
+int item_count(int rows, int unit, int slack, int B) { return kv8::item_count(rows, unit, slack, B); }
+int touched_blocks(int start, int n) { return kv8::touched_blocks(start, n); }
+long long first_unit(long long c, long long U, long long C) { return kv8::first_unit(c, U, C); }
+int worker_of_unit(long long u, long long U, long long C) { return kv8::worker_of_unit(u, U, C); }
+}
