@@ -115,15 +115,24 @@ def _check(status, what):
         raise W4A8Error(status, what)
 
 
+# The current stream's handle: torch.cuda.current_stream() builds a Stream
+# object (2.9 us on the GPU's host) around the handle that this returns (0.1 us).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _p(t):
-    return ctypes.c_void_p(t.data_ptr()) if t is not None else ctypes.c_void_p(0)
+    return t.data_ptr() if t is not None else None
 
 
 def _need(t, dtype, shape, name):
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
@@ -336,21 +345,24 @@ def _need_rows(t, heads, dim, name):
     projection's output will do); returns (tokens, elements between tokens)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.float16:
+    if t.dtype is not torch.float16:
         raise TypeError(f"{name} must be {torch.float16}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"{name} must have shape (tokens, {heads}, {dim}), got {tuple(t.shape)}")
-    n, ld = t.shape[0], t.stride(0)
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        raise ValueError(f"{name} must have shape (tokens, {heads}, {dim}), got {tuple(shape)}")
+    ld, inner, one = t.stride()
+    if one != 1 or (heads > 1 and inner != dim):
         raise ValueError(f"{name}'s heads must be contiguous")
-    return n, ld if n > 1 else heads * dim
+    return shape[0], ld if shape[0] > 1 else heads * dim
 
 
 def prompt_attention(q, k, v, cu_q, cu_k=None, causal=True, scale=None, out=None):
     """Attention of packed prompts: q fp16 [Tq][Hq][D], k and v fp16 [Tk][Hkv][D] (any stride
     between tokens), cu_q and cu_k int32 [B+1] (device; cu_k = cu_q when not given), scale
     1/sqrt(D) when not given -> fp16 [Tq][Hq][D] (w4a8_prompt_attention)."""
-    Hq, D = q.shape[1], q.shape[2]
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q, k and v must have shape (tokens, heads, dim)")
+    _, Hq, D = q.shape
     Hkv = k.shape[1]
     Tq, ld_q = _need_rows(q, Hq, D, "q")
     Tk, ld_k = _need_rows(k, Hkv, D, "k")

@@ -13,17 +13,22 @@
 // pair is written out, the first and the last may be parts of one and go to
 // the workspace (two slots per CTA) for the combine kernel.
 //
-// Tiles.  A warp takes 16 tokens (one scale block) at a time straight from
-// memory into the fragments of mma.sync m16n8k16: the 16 tokens are the rows
-// of S^T = K Q^T, 16 values of d are the rows of O^T = V^T P^T, and 8 query
-// heads are the columns of both, so a group of up to 8 heads wastes nothing
-// that costs.  The order of d inside a product is free, so each lane's
-// 16-byte load (16 codes of one token) is its operand as it stands; for V the
-// codes of two tokens are interleaved by byte permutes.  A code c becomes the
-// exact fp16 value c by placing c + 128 in the mantissa of 1024 and
-// subtracting 1152.  (The tensor memory path needs its operands in shared
-// memory or tensor memory as fp16, which would write and read every code
-// twice more; the products here are 4% of even the mma.sync rate.)
+// Tiles.  A warp takes 16 tokens (one scale block) at a time.  Its own ring of
+// asynchronous copies in shared memory keeps the next blocks' K, V and scales
+// in flight while it works on one: no warp waits for another, and 96 KB or
+// more per SM are on the way, three times what the memory's latency needs at
+// its full rate (registers as the destination, 32 KB per SM, gave 228 us
+// where the ring gives RINGTIME on 682 MB).  The 16 tokens are the rows of
+// S^T = K Q^T, 16 values of d are the rows of O^T = V^T P^T (both mma.sync
+// m16n8k16), and 8 query heads are the columns of both, so a group of up to 8
+// heads wastes nothing that costs.  The order of d inside a product is free,
+// so each lane's 16 bytes of one token (16 codes) are its operand as they
+// stand; for V the codes of two tokens are interleaved by byte permutes.  The
+// copies place 16-byte pieces so that both reads are free of bank conflicts.
+// A code c becomes the exact fp16 value c by placing c + 128 in the mantissa
+// of 1024 and subtracting 1152.  (The tensor memory path needs its operands
+// in shared memory or tensor memory as fp16, which would write and read every
+// code twice more; the products here are 4% of even the mma.sync rate.)
 //
 // Softmax.  x = (scale log2 e s_k) S in fp32.  V's scale goes into the weight:
 // p' = s_v 2^(x - m) multiplies the codes, the running maximum m being of
@@ -36,6 +41,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "kv8.cuh"
+#include "sync.cuh"
 
 namespace {
 
@@ -123,51 +129,55 @@ __device__ long long all_tiles(const DecodeArgs &a, long long *sm) {
     return block_scan(mine, sm, before);
 }
 
-template <int D, int NT>
-struct Tile {
-    static constexpr int KI = D / 64;        // 16-byte loads per token row and lane (K)
-    static constexpr int VW = D / 32;        // 32-bit words per token row and lane (V)
-    uint4 k[2][KI];
-    uint32_t v[4][VW];
-    float ks, vs;
-    bool ok;
+// A warp's ring: S stages of one block each (K, then V, 16 D codes), and the
+// stages' two scales.
+template <int D>
+struct Ring {
+    static constexpr int S = D == 64 ? 6 : 3;
+    static constexpr int HALF = 16 * D;
+    static constexpr int STAGE = 2 * HALF;
+    static constexpr int BYTES = W * S * STAGE;
 };
 
-template <int D, int NT>
-__device__ __forceinline__ void load_k(const DecodeArgs &a, Tile<D, NT> &x, int page, int head, int tok, int g, int t) {
-    x.ok = page >= 0;
-    if (!x.ok) return;
-    const int8_t *p = a.kc + kv8::code_offset(page, a.Hkv, head, a.T, tok, D) + (size_t)g * D + 16 * t;
-    x.ks = a.ks[kv8::scale_offset(page, a.Hkv, head, a.T, tok)];
-    x.vs = a.vs[kv8::scale_offset(page, a.Hkv, head, a.T, tok)];
-#pragma unroll
-    for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int i = 0; i < Tile<D, NT>::KI; ++i) x.k[r][i] = ld_stream_u4(p + 8 * D * r + 64 * i);
+// Byte offset of 16-byte piece c of row r in a block: pieces are permuted
+// within 128 bytes by the row, so that 8 lanes reading the same or
+// neighbouring pieces of several rows meet 8 different bank groups.
+template <int D>
+__device__ __forceinline__ int piece(int r, int c) {
+    if (D == 64) {
+        // two rows to 128 bytes
+        const int f = ((r >> 1) & 3) | ((r & 2) << 1);
+        return (r >> 1) * 128 + ((((r & 1) * 4 + c) ^ f) << 4);
+    }
+    return r * D + (((c & ~7) | ((c ^ r) & 7)) << 4);
 }
 
-// Lane (g, t): tokens 2t, 2t+1, 2t+8, 2t+9; D = 64: 8 codes from 8 g; D = 128:
-// 16 from 16 g; D = 256: 16 from 16 g and 16 from 128 + 16 g.
-template <int D, int NT>
-__device__ __forceinline__ void load_v(const DecodeArgs &a, Tile<D, NT> &x, int page, int head, int tok, int g, int t) {
-    if (page < 0) return;
-    const int8_t *p = a.vc + kv8::code_offset(page, a.Hkv, head, a.T, tok, D) + (size_t)(2 * t) * D + (D == 64 ? 8 : 16) * g;
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+
+// The warp's copies of one block into a stage (dst), its scales into sc.
+template <int D>
+__device__ __forceinline__ void copy_block(const DecodeArgs &a, uint32_t dst, uint32_t sc, int page, int head, int tok, int lane) {
+    constexpr int PR = D / 16;               // pieces per row
+    const size_t at = kv8::code_offset(page, a.Hkv, head, a.T, tok, D);
+    const int8_t *k = a.kc + at, *v = a.vc + at;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const int8_t *pr = p + ((r & 1) + 8 * (r >> 1)) * D;
-        if constexpr (D == 64) {
-            asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(x.v[r][0]), "=r"(x.v[r][1]) : "l"(pr));
-        } else {
-#pragma unroll
-            for (int i = 0; i < D / 128; ++i) {
-                const uint4 w = ld_stream_u4(pr + 128 * i);
-                x.v[r][4 * i] = w.x;
-                x.v[r][4 * i + 1] = w.y;
-                x.v[r][4 * i + 2] = w.z;
-                x.v[r][4 * i + 3] = w.w;
-            }
-        }
+    for (int i = 0; i < PR / 2; ++i) {
+        const int e = lane + 32 * i;
+        const uint32_t to = dst + (uint32_t)piece<D>(e / PR, e % PR);
+        copy16(to, k + 16 * e);
+        copy16(to + Ring<D>::HALF, v + 16 * e);
     }
+    if (lane < 2) copy4(sc + 4 * lane, (lane ? a.vs : a.ks) + kv8::scale_offset(page, a.Hkv, head, a.T, tok));
 }
 
 // d of row `hi` (0: row g, 1: row g + 8) of product tile j for lane group g.
@@ -178,20 +188,52 @@ __device__ __forceinline__ int row_dim(int j, int hi, int g) {
     return (byte >> 4) * 128 + 16 * g + (byte & 15);
 }
 
+// The 16-byte piece of a token's K that lane t's j-th product step uses.
+template <int D>
+__device__ __forceinline__ int k_piece(int t, int j) {
+    return D == 64 ? t : 2 * t + (j & 1) + 8 * (j >> 1);
+}
+
+// V of tokens 2t, 2t+1, 2t+8, 2t+9 for lane (g, t): D = 64: 8 codes from 8 g;
+// D = 128: 16 from 16 g; D = 256: 16 from 16 g and 16 from 128 + 16 g.
+template <int D>
+__device__ __forceinline__ void load_v(uint32_t vb, int g, int t, uint32_t (&v)[4][D / 32]) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int row = 2 * t + (r & 1) + 8 * (r >> 1);
+        if constexpr (D == 64) {
+            asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v[r][0]), "=r"(v[r][1])
+                         : "r"(vb + (uint32_t)(piece<D>(row, g >> 1) + 8 * (g & 1))));
+        } else {
+#pragma unroll
+            for (int i = 0; i < D / 128; ++i) {
+                const uint4 w = lds16(vb + (uint32_t)piece<D>(row, g + 8 * i));
+                v[r][4 * i] = w.x;
+                v[r][4 * i + 1] = w.y;
+                v[r][4 * i + 2] = w.z;
+                v[r][4 * i + 3] = w.w;
+            }
+        }
+    }
+}
+
 // NT: tiles of 8 query heads (1: up to 8 heads per KV head, 2: up to 16).
 template <int D, int NT>
-__global__ void __launch_bounds__(W * 32) kv8_decode_kernel(const DecodeArgs a) {
-    using TL = Tile<D, NT>;
+__global__ void __launch_bounds__(W * 32, D == 256 || NT == 2 ? 1 : 2) kv8_decode_kernel(const DecodeArgs a) {
+    using R = Ring<D>;
     constexpr int NJ = D / 16;            // product tiles of 16 d
     constexpr int NH = 8 * NT;
-    extern __shared__ __align__(16) float sm_o[];            // [W][NH][D]
+    extern __shared__ __align__(128) uint8_t smem[];         // the rings; at a segment's end O [W/2][NH][D]
+    float *sm_o = reinterpret_cast<float *>(smem);
     __shared__ float sm_m[W][NH], sm_l[W][NH];
+    __shared__ float sm_sc[W][R::S][2];
     __shared__ long long sm_scan[32];
     __shared__ int sm_b;
     __shared__ long long sm_u;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * R::S * R::STAGE), ring_sc = smem_u32(&sm_sc[warp][0][0]);
     const long long c = blockIdx.x;
 
     // this CTA's range of units, and the sequence of its first one (no more
@@ -241,7 +283,7 @@ __global__ void __launch_bounds__(W * 32) kv8_decode_kernel(const DecodeArgs a) 
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     uint4 w = make_uint4(0u, 0u, 0u, 0u);
-                    if (8 * n + g < a.G) w = *reinterpret_cast<const uint4 *>(qp + 16 * (t + 4 * i) + 8 * e);
+                    if (8 * n + g < a.G) w = *reinterpret_cast<const uint4 *>(qp + 16 * k_piece<D>(t, i) + 8 * e);
                     qf[n][4 * i + 2 * e][0] = w.x;
                     qf[n][4 * i + 2 * e][1] = w.y;
                     qf[n][4 * i + 2 * e + 1][0] = w.z;
@@ -249,6 +291,7 @@ __global__ void __launch_bounds__(W * 32) kv8_decode_kernel(const DecodeArgs a) 
                 }
         }
 
+        int page_ahead;
         float o[NT][NJ][4], m[NT][2], l[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -260,45 +303,69 @@ __global__ void __launch_bounds__(W * 32) kv8_decode_kernel(const DecodeArgs a) 
             l[n][0] = l[n][1] = 0.0f;
         }
 
-        TL x;
         const int tok_first = first * TILE;
         auto page_of = [&](int i) { return i < nblk ? kv8::page_at(a.table, b, a.maxp, (tok_first + 16 * i) / a.T, a.P) : -1; };
-        int page = page_of(warp);
-        bool bad = warp < nblk && page < 0;
+        // bit s: stage s holds a block (a page that is not there leaves its tokens out)
+        uint32_t there = 0u;
+        bool bad = false;
+        auto issue = [&](int i, int stage, int page) {
+            there &= ~(1u << stage);
+            if (i < nblk) {
+                if (page >= 0) {
+                    copy_block<D>(a, ring + (uint32_t)(stage * R::STAGE), ring_sc + 8u * (uint32_t)stage, page, head, (tok_first + 16 * i) % a.T, lane);
+                    there |= 1u << stage;
+                } else {
+                    bad = true;
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
         {
-            const int tok = (tok_first + 16 * warp) % a.T;
-            load_k<D, NT>(a, x, page, head, tok, g, t);
-            load_v<D, NT>(a, x, page, head, tok, g, t);
+            int pages[R::S];
+#pragma unroll
+            for (int s = 0; s < R::S; ++s) pages[s] = page_of(warp + s * W);
+#pragma unroll
+            for (int s = 0; s < R::S - 1; ++s) issue(warp + s * W, s, pages[s]);
+            page_ahead = pages[R::S - 1];
         }
-        int page_next = page_of(warp + W);
+        int stage = 0;
         for (int i = warp; i < nblk; i += W) {
             const int tok = tok_first + 16 * i;
-            const int tok_next = (tok + 16 * W) % a.T;
-            const bool ok = x.ok;
-            const float ks = x.ks * a.scale_log2, vs = x.vs;
-            float s[NT][4];
+            // the block's copies have landed (all lanes'), and every lane is
+            // done with the stage that is filled next
+            asm volatile("cp.async.wait_group %0;" ::"n"(R::S - 2) : "memory");
+            __syncwarp();
+            issue(i + (R::S - 1) * W, stage == 0 ? R::S - 1 : stage - 1, page_ahead);
+            page_ahead = page_of(i + R::S * W);
+            const bool ok = (there >> stage) & 1u;
+            const uint32_t kb = ring + (uint32_t)(stage * R::STAGE), vb = kb + R::HALF;
+            const float ks = sm_sc[warp][stage][0] * a.scale_log2, vs = sm_sc[warp][stage][1];
+            stage = stage == R::S - 1 ? 0 : stage + 1;
+            float s[NT][4], s2[NT][4];                // two sums: shorter chains of products
 #pragma unroll
-            for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[n][e] = s2[n][e] = 0.0f;
             if (ok) {
 #pragma unroll
-                for (int j = 0; j < TL::KI; ++j) {
-                    const uint32_t lo[4] = {x.k[0][j].x, x.k[0][j].y, x.k[0][j].z, x.k[0][j].w};
-                    const uint32_t hi[4] = {x.k[1][j].x, x.k[1][j].y, x.k[1][j].z, x.k[1][j].w};
+                for (int j = 0; j < D / 64; ++j) {
+                    const int c = k_piece<D>(t, j);
+                    const uint4 kl = lds16(kb + (uint32_t)piece<D>(g, c)), kh = lds16(kb + (uint32_t)piece<D>(g + 8, c));
+                    const uint32_t lo[4] = {kl.x, kl.y, kl.z, kl.w}, hi[4] = {kh.x, kh.y, kh.z, kh.w};
 #pragma unroll
                     for (int w = 0; w < 4; ++w) {
                         const uint32_t p = lo[w] ^ 0x80808080u, r = hi[w] ^ 0x80808080u;
                         const uint32_t a0 = codes_half2<0x4140>(p), a2 = codes_half2<0x4342>(p);
                         const uint32_t a1 = codes_half2<0x4140>(r), a3 = codes_half2<0x4342>(r);
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) mma16816(s[n], a0, a1, a2, a3, qf[n][4 * j + w][0], qf[n][4 * j + w][1]);
+                        for (int n = 0; n < NT; ++n)
+                            mma16816(w & 1 ? s2[n] : s[n], a0, a1, a2, a3, qf[n][4 * j + w][0], qf[n][4 * j + w][1]);
                     }
                 }
-            }
-            // the next tile's K goes out while this one's softmax and second product run
-            const int page_after = page_of(i + 2 * W);
-            if (i + W < nblk) {
-                bad = bad || page_next < 0;
-                load_k<D, NT>(a, x, page_next, head, tok_next, g, t);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[n][e] += s2[n][e];
             }
 
             uint32_t pf[NT][2];
@@ -347,10 +414,12 @@ __global__ void __launch_bounds__(W * 32) kv8_decode_kernel(const DecodeArgs a) 
                     pf[n][0] = transpose8(*reinterpret_cast<const uint32_t *>(&h0));
                     pf[n][1] = transpose8(*reinterpret_cast<const uint32_t *>(&h1));
                 }
+                uint32_t v[4][D / 32];
+                load_v<D>(vb, g, t, v);
 #pragma unroll
-                for (int w = 0; w < TL::VW; ++w) {
-                    const uint32_t v0 = x.v[0][w] ^ 0x80808080u, v1 = x.v[1][w] ^ 0x80808080u;
-                    const uint32_t v2 = x.v[2][w] ^ 0x80808080u, v3 = x.v[3][w] ^ 0x80808080u;
+                for (int w = 0; w < D / 32; ++w) {
+                    const uint32_t v0 = v[0][w] ^ 0x80808080u, v1 = v[1][w] ^ 0x80808080u;
+                    const uint32_t v2 = v[2][w] ^ 0x80808080u, v3 = v[3][w] ^ 0x80808080u;
                     // bytes 0 1 and 2 3 of the four tokens, two tokens side by side
                     const uint32_t p0 = __byte_perm(v0, v1, 0x5140), p1 = __byte_perm(v0, v1, 0x7362);
                     const uint32_t r0 = __byte_perm(v2, v3, 0x5140), r1 = __byte_perm(v2, v3, 0x7362);
@@ -364,9 +433,8 @@ __global__ void __launch_bounds__(W * 32) kv8_decode_kernel(const DecodeArgs a) 
                     }
                 }
             }
-            if (i + W < nblk) load_v<D, NT>(a, x, page_next, head, tok_next, g, t);
-            page_next = page_after;
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
         if (bad && lane == 0) atomicExch(a.status, (int)W4A8_ERR_PAGE);
 
         // merge the warps: M = max m_w, O = sum 2^(m_w - M) O_w, L likewise (warp order)
@@ -381,7 +449,7 @@ __global__ void __launch_bounds__(W * 32) kv8_decode_kernel(const DecodeArgs a) 
                     sm_l[warp][8 * n + 2 * t + e] = l[n][e];
                 }
             }
-        __syncthreads();
+        __syncthreads();                              // also: every warp is done with its ring
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -391,21 +459,42 @@ __global__ void __launch_bounds__(W * 32) kv8_decode_kernel(const DecodeArgs a) 
 #pragma unroll
                 for (int w = 0; w < W; ++w) M = fmaxf(M, sm_m[w][h]);
                 const float f = m[n][e] == -INFINITY ? 0.0f : ex2(m[n][e] - M);
-                float *dst = sm_o + ((size_t)warp * NH + h) * D;
 #pragma unroll
                 for (int j = 0; j < NJ; ++j) {
-                    dst[row_dim<D>(j, 0, g)] = o[n][j][e] * f;
-                    dst[row_dim<D>(j, 1, g)] = o[n][j][e + 2] * f;
+                    o[n][j][e] *= f;
+                    o[n][j][e + 2] *= f;
                 }
             }
-        __syncthreads();
+        // the upper half of the warps hand theirs to the lower half
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            if (warp / (W / 2) == 1 - half) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float *at = sm_o + ((size_t)(warp % (W / 2)) * NH + 8 * n + 2 * t + e) * D;
+#pragma unroll
+                        for (int j = 0; j < NJ; ++j) {
+                            if (half) {
+                                at[row_dim<D>(j, 0, g)] += o[n][j][e];
+                                at[row_dim<D>(j, 1, g)] += o[n][j][e + 2];
+                            } else {
+                                at[row_dim<D>(j, 0, g)] = o[n][j][e];
+                                at[row_dim<D>(j, 1, g)] = o[n][j][e + 2];
+                            }
+                        }
+                    }
+            }
+            __syncthreads();
+        }
         const bool whole = first == 0 && last == nt;
         const int slot = 2 * (int)c + (u == u0 ? 0 : 1);
         for (int i = threadIdx.x; i < a.G * D; i += W * 32) {
             const int h = i / D;
             float v = 0.0f;
 #pragma unroll
-            for (int w = 0; w < W; ++w) v += sm_o[(size_t)w * NH * D + i];
+            for (int w = 0; w < W / 2; ++w) v += sm_o[(size_t)w * NH * D + i];
             float M = -INFINITY, L = 0.0f;
 #pragma unroll
             for (int w = 0; w < W; ++w) M = fmaxf(M, sm_m[w][h]);
@@ -516,16 +605,19 @@ __global__ void __launch_bounds__(NC) kv8_combine_kernel(const DecodeArgs a, int
     }
 }
 
-// CTAs of the split: two per SM, no more than there can be tiles.
-int split_ctas(int B, int Hkv, int T, int maxp) {
+// CTAs of the split: as many as the SMs hold at once (two each where the
+// registers allow it), no more than there can be tiles.
+int split_ctas(int B, int Hq, int Hkv, int D, int T, int maxp) {
     const long long most = (long long)B * Hkv * (((long long)maxp * T + TILE - 1) / TILE);
-    return (int)(most < MAXC ? (most < 1 ? 1 : most) : MAXC);
+    const int fit = D == 256 || Hq / Hkv > 8 ? MAXC / 2 : MAXC;
+    return (int)(most < fit ? (most < 1 ? 1 : most) : fit);
 }
 
 template <int D, int NT>
 w4a8_status launch_decode(const DecodeArgs &a, int C, cudaStream_t stream) {
     static std::atomic<int> attr_done[w4a8_host::kDeviceSlots];
-    const int smem = W * 8 * NT * D * 4;
+    const int smem = Ring<D>::BYTES;
+    static_assert(Ring<D>::BYTES >= W / 2 * 8 * NT * D * 4, "O of half the warps in the rings' space");
     const w4a8_status st = w4a8_host::ensure_smem_limit(kv8_decode_kernel<D, NT>, smem, attr_done);
     if (st != W4A8_OK) return st;
     return w4a8_host::launch_dependent(kv8_decode_kernel<D, NT>, dim3((unsigned)C), W * 32, (size_t)smem, stream, a);
@@ -538,13 +630,13 @@ size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 namespace w4a8_host {
 
 size_t kv8_decode_workspace_bytes(int B, int Hq, int Hkv, int D, int T, int maxp) {
-    const size_t rows = (size_t)2 * split_ctas(B, Hkv, T, maxp) * (Hq / Hkv);
+    const size_t rows = (size_t)2 * split_ctas(B, Hq, Hkv, D, T, maxp) * (Hq / Hkv);
     return align256(rows * D * 4) + rows * 2 * 4;
 }
 
 w4a8_status launch_kv8_decode(const uint16_t *q, const Kv8Cache &c, const int32_t *table, const int32_t *lens, int B,
                               int Hq, int maxp, float scale, uint16_t *out, void *workspace, cudaStream_t stream) {
-    const int C = split_ctas(B, c.Hkv, c.T, maxp), G = Hq / c.Hkv;
+    const int C = split_ctas(B, Hq, c.Hkv, c.D, c.T, maxp), G = Hq / c.Hkv;
     DecodeArgs a = {q, c.k_codes, c.v_codes, c.k_scale, c.v_scale, table, lens, out, static_cast<float *>(workspace),
                     reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + align256((size_t)2 * C * G * c.D * 4)),
                     c.P, c.Hkv, c.T, B, maxp, G, scale * 1.4426950408889634f, device_status_ptr()};
