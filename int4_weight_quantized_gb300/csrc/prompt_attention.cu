@@ -82,6 +82,12 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
     asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
                  ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
@@ -92,6 +98,35 @@ __device__ __forceinline__ void tmem_st_cols16(uint32_t taddr, const uint32_t *v
                  ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
                    "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
                  : "memory");
+}
+
+// One lane of a converged warp (1 there, 0 elsewhere).
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p;
+}
+
+// A value that all lanes hold, as one that the compiler knows to be uniform.
+template <class T>
+__device__ __forceinline__ T uniform(T x) {
+    return __shfl_sync(0xffffffffu, x, 0);
+}
+
+// The tensor-core operations of tc.cuh by the lane where `one` is 1, without a branch.
+__device__ __forceinline__ void tc_mma_f16_if(uint32_t one, uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                 ::"r"(d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc), "r"(one) : "memory");
+}
+__device__ __forceinline__ void tc_mma_f16_ta_if(uint32_t one, uint32_t d, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+                 ::"r"(d), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(acc), "r"(one) : "memory");
+}
+__device__ __forceinline__ void tc_commit_if(uint32_t one, uint32_t bar) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(one) : "memory");
 }
 
 // A wait of one role; false once any wait of the CTA has run out.
@@ -177,12 +212,12 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     const kv8::Rows rq = kv8::sequence_rows(a.cu_q, b, a.Tq), rk = kv8::sequence_rows(a.cu_k, b, a.Tk);
     Job job = {rq.first, rq.n, rk.first, rk.n, (item - kv8::item_base(rq.first, unit, 1, b)) * unit};
     if (job.t0 < 0 || job.t0 >= job.nq) return;              // an idle item (the whole CTA)
-    int n[C::NQ];
+    int steps_of[C::NQ];
     int nmax = 0;
 #pragma unroll
     for (int i = 0; i < C::NQ; ++i) {
-        n[i] = key_steps(job, a, job.t0 + i * a.tok);
-        nmax = max(nmax, n[i]);
+        steps_of[i] = key_steps(job, a, job.t0 + i * a.tok);
+        nmax = max(nmax, steps_of[i]);
     }
 
     if (warp == 0) tmem_alloc_512(smem_u32((const void *)tslot));
@@ -234,99 +269,127 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                 for (int i = 0; i < C::NSLOT; ++i) mbar_wait_bounded(&full[i], i < slot ? phase : phase ^ 1u, a.budget, a.status);
         }
     } else if (warp == W_MMA) {
-        constexpr uint32_t idesc_s = (1u << 4) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
-        constexpr uint32_t idesc_o = (1u << 4) | (1u << 16) | ((uint32_t)(C::SD >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
-        bool ok = true;
-        uint32_t pphase[C::NS] = {};
-        // ring position of a tile's first slot: tiles are used in the order
-        // of their loading, K(0), then V(j), K(j+1) (one row tile: K(j+1), V(j))
-        auto position = [&](bool v, int j) {
-            const int tile = v ? (C::NQ > 1 ? 2 * j + 1 : (j + 1 < nmax ? 2 * j + 2 : 2 * j + 1))
-                               : (j == 0 ? 0 : (C::NQ > 1 ? 2 * j : 2 * j - 1));
-            return tile * C::SPT;
-        };
-        auto s_product = [&](int i, int buf, int j, bool last_use) {
-            if (j == 0) ok = ok && wait.warp(&qbar[i], 0);
-            const int p0 = position(false, j);
-            for (int h = 0; h < C::SPT; ++h) {
-                const int slot = (p0 + h) % C::NSLOT;
-                ok = ok && wait.warp(&full[slot], (uint32_t)((p0 + h) / C::NSLOT) & 1u);
-                if (!ok) return;
-                tc_fence_after();
-                if (lane == 0) {
+        // One lane issues everything; the whole warp walks the ring with it, so
+        // that addresses and descriptors are warp-uniform: an issue then costs few
+        // instructions, and the products keep their pace beside the softmax warps
+        // of this warp's quarter of the SM.
+        {
+            constexpr uint32_t idesc_s = (1u << 4) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+            constexpr uint32_t idesc_o = (1u << 4) | (1u << 16) | ((uint32_t)(C::SD >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+            const uint32_t one = elect_one();
+            const uint32_t tmem = uniform(*tslot), sbase = uniform(smem_u32(smem));
+            const int nk = uniform(job.nk), nmax_u = uniform(nmax);
+            int n[C::NQ];
 #pragma unroll
-                    for (int kk = 0; kk < C::SD / 16; ++kk) {
-                        const int c = kk >> 2, sub = kk & 3;
-                        const uint64_t ad = smem_desc_sw128(sbase + i * C::QTILE + (h * (C::SD / 64) + c) * (128 * 128)) + (uint64_t)(sub * 2);
-                        const uint64_t bd = smem_desc_sw128(sbase + C::OFF_RING + slot * C::SLOT + c * (BN * 128)) + (uint64_t)(sub * 2);
-                        tc_mma_f16(tmem + (uint32_t)(buf * BN), ad, bd, idesc_s, (h > 0 || kk > 0) ? 1u : 0u);
+            for (int i = 0; i < C::NQ; ++i) n[i] = uniform(steps_of[i]);
+            const uint64_t q_desc = smem_desc_sw128(sbase), k_desc = smem_desc_sw128(sbase + C::OFF_RING);
+            const uint64_t v_desc = smem_desc_sw128_mn(sbase + C::OFF_RING, (uint32_t)(BN * 128));
+            const uint32_t bar0 = sbase + (uint32_t)C::OFF_BAR;
+            auto bar_at = [&](const uint64_t *b) { return bar0 + 8u * (uint32_t)(b - bars); };
+            bool ok = true;
+            int slot = 0;
+            uint32_t phase = 0;
+            struct Taken {
+                int slot;
+                uint32_t phase;
+            };
+            auto take = [&]() {                              // the next tile's first slot, in the order of loading
+                const Taken t = {slot, phase};
+                slot += C::SPT;
+                if (slot >= C::NSLOT) {
+                    slot -= C::NSLOT;
+                    phase ^= 1u;
+                }
+                return t;
+            };
+            // slot h of a tile; a tile may run over the ring's end
+            auto part = [&](const Taken &t, int h) {
+                const bool over = t.slot + h >= C::NSLOT;
+                return Taken{over ? t.slot + h - C::NSLOT : t.slot + h, over ? t.phase ^ 1u : t.phase};
+            };
+            auto s_product = [&](int i, int buf, const Taken &tile, bool first_use, bool last_use) {
+#pragma unroll
+                for (int h = 0; h < C::SPT; ++h) {
+                    const Taken t = part(tile, h);
+                    if (first_use) ok = ok && wait.warp(&full[t.slot], t.phase);
+                    if (!ok) return;
+                    tc_fence_after();
+                    const uint64_t ad = q_desc + (uint64_t)((i * C::QTILE + h * (C::SD / 64) * (128 * 128)) >> 4);
+                    const uint64_t bd = k_desc + (uint64_t)(t.slot * (C::SLOT >> 4));
+#pragma unroll
+                    for (int kk = 0; kk < C::SD / 16; ++kk)
+                        tc_mma_f16_if(one, tmem + (uint32_t)(buf * BN), ad + (uint64_t)((kk >> 2) * (128 * 128 >> 4) + (kk & 3) * 2),
+                                   bd + (uint64_t)((kk >> 2) * (BN * 128 >> 4) + (kk & 3) * 2), idesc_s, (h > 0 || kk > 0) ? 1u : 0u);
+                    if (last_use) tc_commit_if(one, bar_at(&empty[0]) + 8u * (uint32_t)t.slot);
+                }
+                tc_commit_if(one, bar_at(&sbar[0]) + 8u * (uint32_t)buf);
+            };
+            auto o_product = [&](int i, int buf, uint32_t pphase, int j, const Taken &tile, bool first_use, bool last_use) {
+                ok = ok && wait.warp(&pbar[buf], pphase);
+                const int groups = (min(BN, nk - j * BN) + 15) / 16;     // of 16 keys that are the sequence's
+                const uint32_t p = tmem + (uint32_t)(buf * BN), acc = j > 0 ? 1u : 0u;
+#pragma unroll
+                for (int h = 0; h < C::SPT; ++h) {
+                    const Taken t = part(tile, h);
+                    if (first_use) ok = ok && wait.warp(&full[t.slot], t.phase);
+                    if (!ok) return;
+                    tc_fence_after();
+                    const uint32_t o = tmem + (uint32_t)(C::COL_O + i * D + h * C::SD);
+                    const uint64_t bd = v_desc + (uint64_t)(t.slot * (C::SLOT >> 4));
+                    if (groups == BN / 16) {
+#pragma unroll
+                        for (int kk = 0; kk < BN / 16; ++kk)
+                            tc_mma_f16_ta_if(one, o, p + (uint32_t)(kk * 8), bd + (uint64_t)(kk * 128), idesc_o, kk > 0 ? 1u : acc);
+                    } else {
+                        for (int kk = 0; kk < groups; ++kk)
+                            tc_mma_f16_ta_if(one, o, p + (uint32_t)(kk * 8), bd + (uint64_t)(kk * 128), idesc_o, kk > 0 ? 1u : acc);
                     }
-                    if (last_use) tc_commit(smem_u32(&empty[slot]));
+                    if (last_use) tc_commit_if(one, bar_at(&empty[0]) + 8u * (uint32_t)t.slot);
                 }
-                __syncwarp();
-            }
-            if (lane == 0) tc_commit(smem_u32(&sbar[buf]));
-            __syncwarp();
-        };
-        auto o_product = [&](int i, int buf, int j, bool first_use, bool last_use) {
-            ok = ok && wait.warp(&pbar[buf], pphase[buf]);
-            pphase[buf] ^= 1u;
-            const int p0 = position(true, j);
-            const int keys = min(BN, job.nk - j * BN);       // of this tile that are the sequence's
-            const int groups = (keys + 15) / 16;
-            for (int h = 0; h < C::SPT; ++h) {
-                const int slot = (p0 + h) % C::NSLOT;
-                ok = ok && wait.warp(&full[slot], (uint32_t)((p0 + h) / C::NSLOT) & 1u);
-                if (!ok) return;
-                if (first_use && (keys & 15)) {
-                    const int row0 = keys, rows = groups * 16 - keys;
-                    for (int x = lane; x < rows * (C::SD / 8); x += 32) {
-                        const int r = row0 + x / (C::SD / 8), q = x % (C::SD / 8);
-                        *reinterpret_cast<uint4 *>(smem + C::OFF_RING + slot * C::SLOT + (q >> 3) * (BN * 128) + r * 128 + (q & 7) * 16) =
-                            make_uint4(0u, 0u, 0u, 0u);
+                tc_commit_if(one, bar_at(&obar[i]));
+                if (j == n[i] - 1) tc_commit_if(one, bar_at(&fbar[i]));
+            };
+            if (nmax_u > 0) {
+                const Taken k0 = take();
+                if constexpr (C::NQ == 1) {
+                    ok = wait.warp(&qbar[0], 0);
+                    s_product(0, 0, k0, true, true);
+                    for (int j = 0; ok && j < nmax_u; ++j) {
+                        if (j + 1 < nmax_u) s_product(0, (j + 1) & 1, take(), true, true);
+                        o_product(0, j & 1, (uint32_t)(j >> 1) & 1u, j, take(), true, true);
                     }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
-                tc_fence_after();
-                if (lane == 0) {
-                    for (int kk = 0; kk < groups; ++kk) {
-                        const uint64_t bd = smem_desc_sw128_mn(sbase + C::OFF_RING + slot * C::SLOT + kk * 16 * 128, (uint32_t)(BN * 128));
-                        tc_mma_f16_ta(tmem + (uint32_t)(C::COL_O + i * D + h * C::SD), tmem + (uint32_t)(buf * BN + kk * 8), bd,
-                                      idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
+                } else {
+                    // the second tile has at least the first one's steps where it has
+                    // tokens at all: it is a slot's last user while it lasts
+                    bool used = false;
+                    for (int i = 0; i < 2; ++i) {
+                        if (n[i] == 0) continue;
+                        ok = ok && wait.warp(&qbar[i], 0);
+                        s_product(i, i, k0, !used, i == 1 || n[1] == 0);
+                        used = true;
                     }
-                    if (last_use) tc_commit(smem_u32(&empty[slot]));
+                    for (int j = 0; ok && j < nmax_u; ++j) {
+                        const Taken v = take();
+                        const Taken k = j + 1 < nmax_u ? take() : v;
+                        bool v_used = false, k_used = false;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            if (j >= n[i]) continue;
+                            o_product(i, i, (uint32_t)j & 1u, j, v, !v_used, i == 1 || j >= n[1]);
+                            v_used = true;
+                            if (j + 1 < n[i]) {
+                                s_product(i, i, k, !k_used, i == 1 || j + 1 >= n[1]);
+                                k_used = true;
+                            }
+                        }
+                    }
                 }
-                __syncwarp();
-            }
-            if (lane == 0) {
-                tc_commit(smem_u32(&obar[i]));
-                if (j == n[i] - 1) tc_commit(smem_u32(&fbar[i]));
-            }
-            __syncwarp();
-        };
-        if constexpr (C::NQ == 1) {
-            if (nmax > 0) s_product(0, 0, 0, true);
-            for (int j = 0; ok && j < nmax; ++j) {
-                if (j + 1 < nmax) s_product(0, (j + 1) & 1, j + 1, true);
-                o_product(0, j & 1, j, true, true);
-            }
-        } else {
-            // the second tile has at least the first one's steps where it has tokens at all
-            auto last = [&](int i, int j) { return i == 1 ? true : j >= n[1]; };
-            for (int i = 0; i < 2; ++i)
-                if (n[i] > 0) s_product(i, i, 0, last(i, 0));
-            for (int j = 0; ok && j < nmax; ++j)
-                for (int i = 0; i < 2; ++i) {
-                    if (j >= n[i]) continue;
-                    o_product(i, i, j, i == 0 || j >= n[0], last(i, j));
-                    if (j + 1 < n[i]) s_product(i, i, j + 1, last(i, j + 1));
+                if (!ok) {
+                    // a wait ran out: what was issued still has to end before the CTA leaves
+                    tc_commit_if(one, bar_at(drain));
+                    mbar_wait_bounded(drain, 0, a.budget, a.status);
                 }
-        }
-        if (!ok && lane == 0) {
-            // a wait ran out: what was issued still has to end before the CTA leaves
-            tc_commit(smem_u32(drain));
-            mbar_wait_bounded(drain, 0, a.budget, a.status);
+            }
         }
         __syncwarp();
     } else {
@@ -337,11 +400,30 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         const int off = job.nk - job.nq;
         const int limit = a.causal ? min(job.nk, tok_i + off + 1) : job.nk;     // keys below it are seen
         const uint32_t ocol = lane_base + (uint32_t)(C::COL_O + grp * D);
-        const int steps = n[grp];
+        const int steps = steps_of[grp];
         // keys that every row of the tile sees: below it no mask is needed
         const int all_see = a.causal ? min(job.nk, job.t0 + grp * a.tok + off + 1) : job.nk;
         float m = -INFINITY, l = 0.0f;
         bool ok = true;
+        auto zero_rows = [&](int j, int keys) {
+            // V(j) is the tile 2 j + 1 of the ring (the last one's place is the same
+            // with one row tile)
+            const int row0 = keys, rows = ((keys + 15) & ~15) - keys;
+            bool w = true;
+#pragma unroll
+            for (int h = 0; h < C::SPT; ++h) {
+                const int at = (2 * j + 1) * C::SPT + h, slot = at % C::NSLOT;
+                w = w && wait.warp(&full[slot], (uint32_t)(at / C::NSLOT) & 1u);
+                if (!w) return false;
+                for (int x = r; x < rows * (C::SD / 8); x += 128) {
+                    const int row = row0 + x / (C::SD / 8), q = x % (C::SD / 8);
+                    *reinterpret_cast<uint4 *>(smem + C::OFF_RING + slot * C::SLOT + (q >> 3) * (BN * 128) + row * 128 + (q & 7) * 16) =
+                        make_uint4(0u, 0u, 0u, 0u);
+                }
+            }
+            fence_proxy_async_smem();
+            return true;
+        };
         for (int j = 0; j < steps; ++j) {
             const int buf = C::NQ == 1 ? (j & 1) : grp;
             const uint32_t ph = C::NQ == 1 ? (uint32_t)(j >> 1) & 1u : (uint32_t)j & 1u;
@@ -360,8 +442,10 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             }
             float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-            for (int c = 4; c < BN; ++c) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+            for (int c = 4; c < BN - 4; c += 2) mx[(c >> 1) & 3] = max3(mx[(c >> 1) & 3], s[c], s[c + 1]);
+            mx[0] = max3(mx[0], s[BN - 4], s[BN - 3]);
+            mx[1] = max3(mx[1], s[BN - 2], s[BN - 1]);
+            const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * a.scale_log2;
             if (__any_sync(0xffffffffu, top > m + 8.0f)) {
                 const float mn = fmaxf(m, top);
                 const float f = m == -INFINITY ? 0.0f : ex2(m - mn);
@@ -404,6 +488,13 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                 tmem_st_cols16(lane_base + (uint32_t)(buf * BN + c * 16), p);
             }
             l += (sum.x + sum.y) + (sum1.x + sum1.y);
+            const int keys = job.nk - j * BN;
+            if (keys < BN && (keys & 15) && (grp == 0 || j >= steps_of[0])) {
+                // the last tile of keys: V's rows from the end to the next 16 become
+                // zero (by the first group that uses the tile, before its P counts)
+                ok = zero_rows(j, keys);
+                if (!ok) break;
+            }
             tmem_st_wait();
             tc_fence_before();
             mbar_arrive(&pbar[buf]);
