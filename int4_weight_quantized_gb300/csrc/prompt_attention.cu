@@ -61,9 +61,14 @@ struct Cfg {
     static constexpr int OFF_RING = NQ * QTILE;
     static constexpr int OFF_BAR = OFF_RING + NSLOT * SLOT;
     static constexpr int SMEM = OFF_BAR + 512 + 1024;        // barriers, slack to align the base
-    static constexpr int COL_O = NS * BN;                    // tensor memory: S buffers, then O
+    // tensor memory: S buffers, O, and P beside S where there is room (then S is
+    // free again as soon as it has been read); else P lies over S
+    static constexpr bool P_BESIDE = D == 64;
+    static constexpr bool K_FIRST = P_BESIDE || NQ == 1;     // S(j + 1) is computed before P(j) V(j)
+    static constexpr int COL_O = NS * BN;
+    static constexpr int COL_P = COL_O + NQ * D;
     static_assert(SMEM <= 227 * 1024, "shared memory");
-    static_assert(COL_O + NQ * D <= 512, "tensor memory");
+    static_assert(COL_P + (P_BESIDE ? NQ * BN / 2 : 0) <= 512, "tensor memory");
 };
 
 struct PromptArgs {
@@ -173,12 +178,13 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
     uint64_t *qbar = bars;                       // [NQ]
     uint64_t *sbar = bars + 2;                   // [NS] S written
-    uint64_t *pbar = bars + 4;                   // [NS] P written (128 threads), S read
-    uint64_t *obar = bars + 6;                   // [NQ] product of the step added to O
-    uint64_t *drain = bars + 8 + 2 * C::NSLOT;
-    uint64_t *fbar = bars + 9 + 2 * C::NSLOT;    // [NQ] O complete
-    uint64_t *full = bars + 8, *empty = bars + 8 + C::NSLOT;
-    volatile uint32_t *tslot = reinterpret_cast<volatile uint32_t *>(bars + 11 + 2 * C::NSLOT);
+    uint64_t *pbar = bars + 4;                   // [2][NS] half of P written (128 threads)
+    uint64_t *rbar = bars + 8;                   // [NQ] S read (128 threads; where P lies beside it)
+    uint64_t *obar = bars + 10;                  // [NQ] product of the step added to O
+    uint64_t *fbar = bars + 12;                  // [NQ] O complete
+    uint64_t *drain = bars + 14;
+    uint64_t *full = bars + 15, *empty = full + C::NSLOT;
+    volatile uint32_t *tslot = reinterpret_cast<volatile uint32_t *>(empty + C::NSLOT);
     volatile uint32_t *abort_flag = tslot + 1;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -188,10 +194,12 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         for (int i = 0; i < C::NS; ++i) {
             mbar_init(&sbar[i], 1);
             mbar_init(&pbar[i], 128);
+            mbar_init(&pbar[C::NS + i], 128);
         }
         for (int i = 0; i < C::NQ; ++i) {
             mbar_init(&obar[i], 1);
             mbar_init(&fbar[i], 1);
+            mbar_init(&rbar[i], 128);
         }
         for (int i = 0; i < C::NSLOT; ++i) {
             mbar_init(&full[i], 1);
@@ -259,9 +267,9 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             load_tile(&tm_k, 0);
             for (int i = 1; i < C::NQ; ++i) load_q(i);
             for (int j = 0; j < nmax; ++j) {
-                if (C::NQ == 1 && j + 1 < nmax) load_tile(&tm_k, j + 1);
+                if (C::K_FIRST && j + 1 < nmax) load_tile(&tm_k, j + 1);
                 load_tile(&tm_v, j);
-                if (C::NQ > 1 && j + 1 < nmax) load_tile(&tm_k, j + 1);
+                if (!C::K_FIRST && j + 1 < nmax) load_tile(&tm_k, j + 1);
             }
             // no copy is in flight when the CTA leaves: Q's, and every slot's last
             for (int i = 0; i < C::NQ; ++i) mbar_wait_bounded(&qbar[i], 0, a.budget, a.status);
@@ -324,27 +332,36 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                 }
                 tc_commit_if(one, bar_at(&sbar[0]) + 8u * (uint32_t)buf);
             };
+            // O += P V in two halves of the keys, each as soon as its P is there
             auto o_product = [&](int i, int buf, uint32_t pphase, int j, const Taken &tile, bool first_use, bool last_use) {
-                ok = ok && wait.warp(&pbar[buf], pphase);
                 const int groups = (min(BN, nk - j * BN) + 15) / 16;     // of 16 keys that are the sequence's
-                const uint32_t p = tmem + (uint32_t)(buf * BN), acc = j > 0 ? 1u : 0u;
+                const uint32_t p = tmem + (uint32_t)(C::P_BESIDE ? C::COL_P + i * (BN / 2) : buf * BN);
 #pragma unroll
-                for (int h = 0; h < C::SPT; ++h) {
-                    const Taken t = part(tile, h);
-                    if (first_use) ok = ok && wait.warp(&full[t.slot], t.phase);
-                    if (!ok) return;
-                    tc_fence_after();
-                    const uint32_t o = tmem + (uint32_t)(C::COL_O + i * D + h * C::SD);
-                    const uint64_t bd = v_desc + (uint64_t)(t.slot * (C::SLOT >> 4));
-                    if (groups == BN / 16) {
+                for (int half = 0; half < 2; ++half) {
+                    ok = ok && wait.warp(&pbar[half * C::NS + buf], pphase);
 #pragma unroll
-                        for (int kk = 0; kk < BN / 16; ++kk)
-                            tc_mma_f16_ta_if(one, o, p + (uint32_t)(kk * 8), bd + (uint64_t)(kk * 128), idesc_o, kk > 0 ? 1u : acc);
-                    } else {
-                        for (int kk = 0; kk < groups; ++kk)
-                            tc_mma_f16_ta_if(one, o, p + (uint32_t)(kk * 8), bd + (uint64_t)(kk * 128), idesc_o, kk > 0 ? 1u : acc);
+                    for (int h = 0; h < C::SPT; ++h) {
+                        const Taken t = part(tile, h);
+                        if (first_use && half == 0) ok = ok && wait.warp(&full[t.slot], t.phase);
+                        if (!ok) return;
+                        tc_fence_after();
+                        const uint32_t o = tmem + (uint32_t)(C::COL_O + i * D + h * C::SD);
+                        const uint64_t bd = v_desc + (uint64_t)(t.slot * (C::SLOT >> 4));
+                        const uint32_t acc = half > 0 || j > 0 ? 1u : 0u;
+                        if (groups == BN / 16) {
+#pragma unroll
+                            for (int k = 0; k < BN / 32; ++k) {
+                                const int kk = half * (BN / 32) + k;
+                                tc_mma_f16_ta_if(one, o, p + (uint32_t)(kk * 8), bd + (uint64_t)(kk * 128), idesc_o, k > 0 ? 1u : acc);
+                            }
+                        } else {
+                            for (int k = 0; k < BN / 32 && half * (BN / 32) + k < groups; ++k) {
+                                const int kk = half * (BN / 32) + k;
+                                tc_mma_f16_ta_if(one, o, p + (uint32_t)(kk * 8), bd + (uint64_t)(kk * 128), idesc_o, k > 0 ? 1u : acc);
+                            }
+                        }
+                        if (last_use && half == 1) tc_commit_if(one, bar_at(&empty[0]) + 8u * (uint32_t)t.slot);
                     }
-                    if (last_use) tc_commit_if(one, bar_at(&empty[0]) + 8u * (uint32_t)t.slot);
                 }
                 tc_commit_if(one, bar_at(&obar[i]));
                 if (j == n[i] - 1) tc_commit_if(one, bar_at(&fbar[i]));
@@ -369,15 +386,26 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                         used = true;
                     }
                     for (int j = 0; ok && j < nmax_u; ++j) {
-                        const Taken v = take();
-                        const Taken k = j + 1 < nmax_u ? take() : v;
+                        // (K(j + 1) is loaded before V(j) where S does not wait for P)
+                        const Taken a1 = take();
+                        const Taken a2 = j + 1 < nmax_u ? take() : a1;
+                        const Taken v = C::P_BESIDE ? a2 : a1, k = C::P_BESIDE ? a1 : a2;
                         bool v_used = false, k_used = false;
+                        if constexpr (C::P_BESIDE) {
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                if (j + 1 >= n[i]) continue;
+                                ok = ok && wait.warp(&rbar[i], (uint32_t)j & 1u);
+                                s_product(i, i, k, !k_used, i == 1 || j + 1 >= n[1]);
+                                k_used = true;
+                            }
+                        }
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             if (j >= n[i]) continue;
                             o_product(i, i, (uint32_t)j & 1u, j, v, !v_used, i == 1 || j >= n[1]);
                             v_used = true;
-                            if (j + 1 < n[i]) {
+                            if (!C::P_BESIDE && j + 1 < n[i]) {
                                 s_product(i, i, k, !k_used, i == 1 || j + 1 >= n[1]);
                                 k_used = true;
                             }
@@ -406,8 +434,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         float m = -INFINITY, l = 0.0f;
         bool ok = true;
         auto zero_rows = [&](int j, int keys) {
-            // V(j) is the tile 2 j + 1 of the ring (the last one's place is the same
-            // with one row tile)
+            // the last V is the tile 2 j + 1 of the ring in either order of loading
             const int row0 = keys, rows = ((keys + 15) & ~15) - keys;
             bool w = true;
 #pragma unroll
@@ -427,6 +454,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         for (int j = 0; j < steps; ++j) {
             const int buf = C::NQ == 1 ? (j & 1) : grp;
             const uint32_t ph = C::NQ == 1 ? (uint32_t)(j >> 1) & 1u : (uint32_t)j & 1u;
+            const uint32_t pcol = lane_base + (uint32_t)(C::P_BESIDE ? C::COL_P + grp * (BN / 2) : buf * BN);
             ok = wait.warp(&sbar[buf], ph);
             if (!ok) break;
             tc_fence_after();
@@ -434,6 +462,10 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
 #pragma unroll
             for (int c = 0; c < BN / 32; ++c) tmem_ld_cols<32>(lane_base + (uint32_t)(buf * BN + c * 32), sr + 32 * c);
             tmem_ld_wait();
+            if constexpr (C::P_BESIDE) {
+                tc_fence_before();
+                mbar_arrive(&rbar[grp]);                     // S is in registers
+            }
             float *s = reinterpret_cast<float *>(sr);
             if ((j + 1) * BN > all_see) {
                 const int lim = limit - j * BN;
@@ -468,6 +500,21 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                     }
                 }
             }
+            if constexpr (C::P_BESIDE) {
+                // P's place is free once the last step's product is in
+                if (j > 0) {
+                    ok = wait.warp(&obar[grp], (uint32_t)(j - 1) & 1u);
+                    if (!ok) break;
+                    tc_fence_after();
+                }
+            }
+            const int keys = job.nk - j * BN;
+            if (keys < BN && (keys & 15) && (grp == 0 || j >= steps_of[0])) {
+                // the last tile of keys: V's rows from the end to the next 16 become
+                // zero (by the first group that uses the tile, before its P counts)
+                ok = zero_rows(j, keys);
+                if (!ok) break;
+            }
             const float mb = m == -INFINITY ? 0.0f : -m;
             const float2 sc2 = make_float2(a.scale_log2, a.scale_log2), mb2 = make_float2(mb, mb);
             float2 sum = make_float2(0.0f, 0.0f), sum1 = sum;
@@ -485,19 +532,17 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                     const __half2 h = __floats2half2_rn(x.x, x.y);
                     p[e] = *reinterpret_cast<const uint32_t *>(&h);
                 }
-                tmem_st_cols16(lane_base + (uint32_t)(buf * BN + c * 16), p);
+                tmem_st_cols16(pcol + (uint32_t)(c * 16), p);
+                if (c == BN / 64 - 1) {
+                    tmem_st_wait();
+                    tc_fence_before();
+                    mbar_arrive(&pbar[buf]);
+                }
             }
             l += (sum.x + sum.y) + (sum1.x + sum1.y);
-            const int keys = job.nk - j * BN;
-            if (keys < BN && (keys & 15) && (grp == 0 || j >= steps_of[0])) {
-                // the last tile of keys: V's rows from the end to the next 16 become
-                // zero (by the first group that uses the tile, before its P counts)
-                ok = zero_rows(j, keys);
-                if (!ok) break;
-            }
             tmem_st_wait();
             tc_fence_before();
-            mbar_arrive(&pbar[buf]);
+            mbar_arrive(&pbar[C::NS + buf]);
         }
         // (a barrier of its own: with one row tile the last two products may both
         // be under way, and obar's parity does not tell a phase from the one two
