@@ -49,12 +49,14 @@ constexpr int BN = 128;              // keys per step
 
 template <int D>
 struct Cfg {
-    static constexpr int NQ = D <= 128 ? 2 : 1;              // row tiles per CTA
-    static constexpr int NS = 2;                             // S buffers
+    static constexpr int NQ = D == 128 ? 2 : 1;              // row tiles per CTA
+    static constexpr int NS = D == 64 ? 1 : 2;               // S buffers
+    static constexpr int CTAS = D == 64 ? 2 : 1;             // per SM
+    static constexpr int TCOLS = 512 / CTAS;                 // tensor memory columns
     static constexpr int SD = D < 128 ? D : 128;             // dims per ring slot
     static constexpr int SPT = D / SD;                       // slots per K or V tile
     static constexpr int SLOT = BN * SD * 2;
-    static constexpr int NSLOT = D == 64 ? 10 : 5;
+    static constexpr int NSLOT = 5;
     static constexpr int QTILE = 128 * D * 2;
     static constexpr int GROUPS = NQ;                        // softmax groups of 4 warps
     static constexpr int THREADS = (4 * GROUPS + 2) * 32;
@@ -64,11 +66,11 @@ struct Cfg {
     // tensor memory: S buffers, O, and P beside S where there is room (then S is
     // free again as soon as it has been read); else P lies over S
     static constexpr bool P_BESIDE = D == 64;
-    static constexpr bool K_FIRST = P_BESIDE || NQ == 1;     // S(j + 1) is computed before P(j) V(j)
+    static constexpr bool K_FIRST = NQ == 1;                 // S(j + 1) is computed before P(j) V(j)
     static constexpr int COL_O = NS * BN;
     static constexpr int COL_P = COL_O + NQ * D;
-    static_assert(SMEM <= 227 * 1024, "shared memory");
-    static_assert(COL_P + (P_BESIDE ? NQ * BN / 2 : 0) <= 512, "tensor memory");
+    static_assert((SMEM + 1024) * CTAS <= 228 * 1024, "shared memory");
+    static_assert(COL_P + (P_BESIDE ? NQ * BN / 2 : 0) <= TCOLS, "tensor memory");
 };
 
 struct PromptArgs {
@@ -167,7 +169,7 @@ __device__ __forceinline__ int key_steps(const Job &j, const PromptArgs &a, int 
 }
 
 template <int D>
-__global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
+__global__ void __launch_bounds__(Cfg<D>::THREADS, Cfg<D>::CTAS)
 prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const PromptArgs a) {
     using C = Cfg<D>;
@@ -228,7 +230,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         nmax = max(nmax, steps_of[i]);
     }
 
-    if (warp == 0) tmem_alloc_512(smem_u32((const void *)tslot));
+    if (warp == 0) tmem_alloc_cols(smem_u32((const void *)tslot), C::TCOLS);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -372,8 +374,12 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                     ok = wait.warp(&qbar[0], 0);
                     s_product(0, 0, k0, true, true);
                     for (int j = 0; ok && j < nmax_u; ++j) {
-                        if (j + 1 < nmax_u) s_product(0, (j + 1) & 1, take(), true, true);
-                        o_product(0, j & 1, (uint32_t)(j >> 1) & 1u, j, take(), true, true);
+                        if (j + 1 < nmax_u) {
+                            // one S buffer: as soon as it has been read
+                            if (C::NS == 1) ok = wait.warp(&rbar[0], (uint32_t)j & 1u);
+                            s_product(0, (j + 1) % C::NS, take(), true, true);
+                        }
+                        o_product(0, j % C::NS, (uint32_t)(j / C::NS) & 1u, j, take(), true, true);
                     }
                 } else {
                     // the second tile has at least the first one's steps where it has
@@ -386,26 +392,15 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                         used = true;
                     }
                     for (int j = 0; ok && j < nmax_u; ++j) {
-                        // (K(j + 1) is loaded before V(j) where S does not wait for P)
-                        const Taken a1 = take();
-                        const Taken a2 = j + 1 < nmax_u ? take() : a1;
-                        const Taken v = C::P_BESIDE ? a2 : a1, k = C::P_BESIDE ? a1 : a2;
+                        const Taken v = take();
+                        const Taken k = j + 1 < nmax_u ? take() : v;
                         bool v_used = false, k_used = false;
-                        if constexpr (C::P_BESIDE) {
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                if (j + 1 >= n[i]) continue;
-                                ok = ok && wait.warp(&rbar[i], (uint32_t)j & 1u);
-                                s_product(i, i, k, !k_used, i == 1 || j + 1 >= n[1]);
-                                k_used = true;
-                            }
-                        }
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             if (j >= n[i]) continue;
                             o_product(i, i, (uint32_t)j & 1u, j, v, !v_used, i == 1 || j >= n[1]);
                             v_used = true;
-                            if (!C::P_BESIDE && j + 1 < n[i]) {
+                            if (j + 1 < n[i]) {
                                 s_product(i, i, k, !k_used, i == 1 || j + 1 >= n[1]);
                                 k_used = true;
                             }
@@ -452,8 +447,8 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             return true;
         };
         for (int j = 0; j < steps; ++j) {
-            const int buf = C::NQ == 1 ? (j & 1) : grp;
-            const uint32_t ph = C::NQ == 1 ? (uint32_t)(j >> 1) & 1u : (uint32_t)j & 1u;
+            const int buf = C::NQ == 1 ? j % C::NS : grp;
+            const uint32_t ph = (uint32_t)(C::NQ == 1 ? j / C::NS : j) & 1u;
             const uint32_t pcol = lane_base + (uint32_t)(C::P_BESIDE ? C::COL_P + grp * (BN / 2) : buf * BN);
             ok = wait.warp(&sbar[buf], ph);
             if (!ok) break;
@@ -579,7 +574,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     __syncthreads();
     if (warp == 0) {
         tc_fence_after();
-        tmem_dealloc_512(tmem);
+        tmem_dealloc_cols(tmem, C::TCOLS);
     }
 }
 
