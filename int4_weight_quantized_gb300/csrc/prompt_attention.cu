@@ -95,6 +95,10 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return y;
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
     asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
                  ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
@@ -211,7 +215,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         *abort_flag = 0u;
         fence_barrier_init();
     }
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (warp == W_TMA && lane < 3) prefetch_map(lane == 0 ? &tm_q : lane == 1 ? &tm_k : &tm_v);
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
     // the heaviest items (the last tokens of a sequence) come first
@@ -230,10 +234,14 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         nmax = max(nmax, steps_of[i]);
     }
 
+    // Tensor memory is taken after the kernel before this one has ended and
+    // before the next one may begin: two kernels on an SM that each hold some
+    // while waiting for the other would wait forever.
     if (warp == 0) tmem_alloc_cols(smem_u32((const void *)tslot), C::TCOLS);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint32_t tmem = *tslot;
     const Waiter wait = {abort_flag, a.budget, a.status};
 
