@@ -7,11 +7,12 @@
 // of its group: the bytes of the cache are the time.
 //
 // Split.  The (sequence, KV head) pairs' 64-token tiles are numbered in order
-// and cut into equal ranges, one per CTA, wherever the cuts fall: long and
-// short sequences balance, one long sequence spreads over the whole GPU.  A
-// CTA's range is a run of segments (one per pair); a segment that is a whole
-// pair is written out, the first and the last may be parts of one and go to
-// the workspace (two slots per CTA) for the combine kernel.
+// and cut into equal ranges, one per warp, wherever the cuts fall: long and
+// short sequences balance, one long sequence spreads over the whole GPU, and
+// no warp waits for another.  A warp's range is a run of segments (one per
+// pair); a segment that is a whole pair is written out, the first and the last
+// may be parts of one and go to the workspace (two slots per warp) for the
+// combine kernel.
 //
 // Tiles.  A warp takes 16 tokens (one scale block) at a time.  Its own ring of
 // asynchronous copies in shared memory keeps the next blocks' K, V and scales
@@ -50,6 +51,7 @@ using namespace w4a8;
 constexpr int W = 8;                 // warps per CTA
 constexpr int TILE = 64;             // tokens per unit of the split
 constexpr int MAXC = 152 * 2;        // CTAs at most
+constexpr int MAXW = MAXC * W;       // workers (warps) at most
 constexpr float kTiny = 8.673617e-19f;   // 2^-60: stands for a zero scale in the weights (the smallest
                                          // real one, from the smallest fp16 value, is 2^-31)
 
@@ -59,8 +61,9 @@ struct DecodeArgs {
     const float *ks, *vs;
     const int32_t *table, *lens;
     uint16_t *out;
-    float *ws_o, *ws_ml;             // [2 C][G][D], [2 C][G][2]
-    int P, Hkv, T, B, maxp, G;
+    float *ws_o, *ws_ml;             // two slots per worker: [G][D], [G][2]
+    int2 *ws_parts;                  // [B][Hkv]: a pair's first slot, and how many workers have a part of it
+    int P, Hkv, T, T_log2, B, maxp, G;
     float scale_log2;                // scale * log2(e)
     int *status;
 };
@@ -68,6 +71,19 @@ struct DecodeArgs {
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// (both approximate: an error of p' is one of the weight and of its part of the
+// sum alike, and 2^-22 of it at most)
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 
@@ -122,11 +138,39 @@ __device__ __forceinline__ long long block_scan(long long v, long long *sm, long
     return total;
 }
 
-// All sequences' tiles (of one KV head).
-__device__ long long all_tiles(const DecodeArgs &a, long long *sm) {
-    long long mine = 0, before;
-    for (int b = threadIdx.x; b < a.B; b += blockDim.x) mine += seq_tiles(a, b);
-    return block_scan(mine, sm, before);
+// Where a warp is in its range of units: the current segment's pair and blocks.
+struct Cursor {
+    long long ub;                    // first unit of sequence b
+    int b, head, nt, len;            // the pair; the sequence's tiles (of one head) and length
+    int blk, end;                    // next block of 16 tokens, and the segment's end
+    int first, last;                 // its tiles
+};
+
+// The segment that begins at unit u of the pair the cursor is at or behind
+// (the sequence is found by walking on from c.b; u1: the range's end).
+__device__ __forceinline__ void set_segment(const DecodeArgs &a, Cursor &c, long long u, long long u1) {
+    const int first = (int)(u - c.ub - (long long)c.head * c.nt);
+    const int last = (int)min((long long)c.nt, first + (u1 - u));
+    c.first = first;
+    c.last = last;
+    c.blk = first * (TILE / 16);
+    c.end = (min(c.len, last * TILE) + 15) >> 4;
+}
+
+// On to the next pair; false at the range's end.
+__device__ __forceinline__ bool next_segment(const DecodeArgs &a, Cursor &c, long long u1) {
+    const long long u = c.ub + (long long)c.head * c.nt + c.last;
+    if (u >= u1) return false;
+    if (++c.head == a.Hkv) {
+        c.head = 0;
+        do {
+            c.ub += (long long)c.nt * a.Hkv;
+            c.len = seq_len(a, ++c.b);
+            c.nt = (c.len + TILE - 1) / TILE;
+        } while (c.nt == 0);
+    }
+    set_segment(a, c, u, u1);
+    return true;
 }
 
 // A warp's ring: S stages of one block each (K, then V, 16 D codes), and the
@@ -168,7 +212,7 @@ __device__ __forceinline__ uint4 lds16(uint32_t a) {
 template <int D>
 __device__ __forceinline__ void copy_block(const DecodeArgs &a, uint32_t dst, uint32_t sc, int page, int head, int tok, int lane) {
     constexpr int PR = D / 16;               // pieces per row
-    const size_t at = kv8::code_offset(page, a.Hkv, head, a.T, tok, D);
+    const size_t at = ((((size_t)page * a.Hkv + head) << a.T_log2) + tok) * D;
     const int8_t *k = a.kc + at, *v = a.vc + at;
 #pragma unroll
     for (int i = 0; i < PR / 2; ++i) {
@@ -177,7 +221,7 @@ __device__ __forceinline__ void copy_block(const DecodeArgs &a, uint32_t dst, ui
         copy16(to, k + 16 * e);
         copy16(to + Ring<D>::HALF, v + 16 * e);
     }
-    if (lane < 2) copy4(sc + 4 * lane, (lane ? a.vs : a.ks) + kv8::scale_offset(page, a.Hkv, head, a.T, tok));
+    if (lane < 2) copy4(sc + 4 * lane, (lane ? a.vs : a.ks) + ((((size_t)page * a.Hkv + head) << a.T_log2) + tok) / kv8::kBlockTokens);
 }
 
 // d of row `hi` (0: row g, 1: row g + 8) of product tile j for lane group g.
@@ -222,62 +266,81 @@ template <int D, int NT>
 __global__ void __launch_bounds__(W * 32, D == 256 || NT == 2 ? 1 : 2) kv8_decode_kernel(const DecodeArgs a) {
     using R = Ring<D>;
     constexpr int NJ = D / 16;            // product tiles of 16 d
-    constexpr int NH = 8 * NT;
-    extern __shared__ __align__(128) uint8_t smem[];         // the rings; at a segment's end O [W/2][NH][D]
-    float *sm_o = reinterpret_cast<float *>(smem);
-    __shared__ float sm_m[W][NH], sm_l[W][NH];
+    extern __shared__ __align__(128) uint8_t smem[];         // the warps' rings
     __shared__ float sm_sc[W][R::S][2];
-    __shared__ long long sm_scan[32];
-    __shared__ int sm_b;
-    __shared__ long long sm_u;
+    __shared__ long long sm_scan[W * 32];
+    __shared__ long long sm_part[W];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * R::S * R::STAGE), ring_sc = smem_u32(&sm_sc[warp][0][0]);
-    const long long c = blockIdx.x;
 
-    // this CTA's range of units, and the sequence of its first one (no more
-    // workers than units: every worker of a pair then has a part of it)
-    const long long U = all_tiles(a, sm_scan) * a.Hkv, C = min((long long)gridDim.x, U);
+    // thread i sums the tiles of its share of the sequences; the shares' starts
+    // in units go to shared memory
+    const int share = (a.B + W * 32 - 1) / (W * 32);
+    long long mine = 0, before;
+    for (int i = 0; i < share; ++i) {
+        const int sb = threadIdx.x * share + i;
+        if (sb < a.B) mine += seq_tiles(a, sb);
+    }
+    const long long U = block_scan(mine, sm_part, before) * a.Hkv;
+    sm_scan[threadIdx.x] = before * a.Hkv;
+    __syncthreads();
+    // this warp's range (no more workers than units: every worker of a pair
+    // then has a part of it); neighbours in the order are on different SMs
+    const long long C = min((long long)gridDim.x * W, U), c = (long long)warp * gridDim.x + blockIdx.x;
     if (c >= C) return;
     const long long u0 = kv8::first_unit(c, U, C), u1 = kv8::first_unit(c + 1, U, C);
+    Cursor put;                           // the block that is copied next
     {
-        long long done = 0;
-        for (int b0 = 0; b0 < a.B; b0 += blockDim.x) {
-            const int b = b0 + threadIdx.x;
-            const long long mine = b < a.B ? (long long)seq_tiles(a, b) * a.Hkv : 0;
-            long long before;
-            const long long total = block_scan(mine, sm_scan, before);
-            if (u0 >= done + before && u0 < done + before + mine) {
-                sm_b = b;
-                sm_u = done + before;
-            }
-            done += total;
-            if (done > u0) break;
+        int at = 0;
+#pragma unroll
+        for (int i = 0; i < W; ++i) at += __popc(__ballot_sync(0xffffffffu, sm_scan[i * 32 + lane] <= u0));
+        put.b = (at - 1) * share;         // the last share that begins at or before u0
+        put.ub = sm_scan[at - 1];
+        put.len = seq_len(a, put.b);
+        put.nt = (put.len + TILE - 1) / TILE;
+        while (u0 >= put.ub + (long long)put.nt * a.Hkv) {
+            put.ub += (long long)put.nt * a.Hkv;
+            put.len = seq_len(a, ++put.b);
+            put.nt = (put.len + TILE - 1) / TILE;
         }
+        put.head = (int)((u0 - put.ub) / put.nt);
+        set_segment(a, put, u0, u1);
     }
-    __syncthreads();
-    int b = sm_b;
-    long long ub = sm_u;                  // first unit of sequence b
-
-    for (long long u = u0; u < u1;) {
-        int nt = seq_tiles(a, b);
-        while (u >= ub + (long long)nt * a.Hkv) {
-            ub += (long long)nt * a.Hkv;
-            nt = seq_tiles(a, ++b);
+    Cursor get = put;                     // the block that is worked on next
+    bool more = true;                     // put is at a block
+    // bit s: stage s holds a block (a page that is not there leaves its tokens out)
+    uint32_t there = 0u;
+    bool bad = false;
+    auto page_of = [&](const Cursor &x) { return kv8::page_at(a.table, x.b, a.maxp, (x.blk * 16) >> a.T_log2, a.P); };
+    int page = page_of(put);              // looked up a step ahead of its use
+    auto issue = [&](int stage) {
+        there &= ~(1u << stage);
+        if (more) {
+            if (page >= 0) {
+                copy_block<D>(a, ring + (uint32_t)(stage * R::STAGE), ring_sc + 8u * (uint32_t)stage, page, put.head,
+                              (put.blk * 16) & (a.T - 1), lane);
+                there |= 1u << stage;
+            } else {
+                bad = true;
+            }
+            if (++put.blk == put.end) more = next_segment(a, put, u1);
+            if (more) page = page_of(put);
         }
-        const int head = (int)((u - ub) / nt);
-        const long long us = ub + (long long)head * nt;      // the pair's units: us .. us + nt - 1
-        const int first = (int)(u - us), last = (int)(min(u1, us + nt) - us);
-        const int len = seq_len(a, b);
-        const int tok_end = min(len, last * TILE);
-        const int nblk = (tok_end - first * TILE + 15) / 16;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int s = 0; s < R::S - 1; ++s) issue(s);
+    int stage = 0;
 
-        // q as the products' B operand: head g of each tile of 8 (zero past the group)
+    while (true) {
+        // a segment: q as the products' B operand, head g of each tile of 8 (zero past the group)
         uint32_t qf[NT][D / 16][2];
+        const size_t row0 = ((size_t)get.b * a.Hkv + get.head) * (size_t)a.G;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const uint16_t *qp = a.q + ((size_t)b * a.Hkv + head) * (size_t)a.G * D + (size_t)(8 * n + g) * D;
+            const uint16_t *qp = a.q + (row0 + 8 * n + g) * D;
 #pragma unroll
             for (int i = 0; i < D / 64; ++i)
 #pragma unroll
@@ -290,8 +353,6 @@ __global__ void __launch_bounds__(W * 32, D == 256 || NT == 2 ? 1 : 2) kv8_decod
                     qf[n][4 * i + 2 * e + 1][1] = w.w;
                 }
         }
-
-        int page_ahead;
         float o[NT][NJ][4], m[NT][2], l[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -303,40 +364,13 @@ __global__ void __launch_bounds__(W * 32, D == 256 || NT == 2 ? 1 : 2) kv8_decod
             l[n][0] = l[n][1] = 0.0f;
         }
 
-        const int tok_first = first * TILE;
-        auto page_of = [&](int i) { return i < nblk ? kv8::page_at(a.table, b, a.maxp, (tok_first + 16 * i) / a.T, a.P) : -1; };
-        // bit s: stage s holds a block (a page that is not there leaves its tokens out)
-        uint32_t there = 0u;
-        bool bad = false;
-        auto issue = [&](int i, int stage, int page) {
-            there &= ~(1u << stage);
-            if (i < nblk) {
-                if (page >= 0) {
-                    copy_block<D>(a, ring + (uint32_t)(stage * R::STAGE), ring_sc + 8u * (uint32_t)stage, page, head, (tok_first + 16 * i) % a.T, lane);
-                    there |= 1u << stage;
-                } else {
-                    bad = true;
-                }
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-        };
-        {
-            int pages[R::S];
-#pragma unroll
-            for (int s = 0; s < R::S; ++s) pages[s] = page_of(warp + s * W);
-#pragma unroll
-            for (int s = 0; s < R::S - 1; ++s) issue(warp + s * W, s, pages[s]);
-            page_ahead = pages[R::S - 1];
-        }
-        int stage = 0;
-        for (int i = warp; i < nblk; i += W) {
-            const int tok = tok_first + 16 * i;
+        for (; get.blk < get.end; ++get.blk) {
+            const int left = get.len - get.blk * 16;         // tokens from the block's first
             // the block's copies have landed (all lanes'), and every lane is
             // done with the stage that is filled next
             asm volatile("cp.async.wait_group %0;" ::"n"(R::S - 2) : "memory");
             __syncwarp();
-            issue(i + (R::S - 1) * W, stage == 0 ? R::S - 1 : stage - 1, page_ahead);
-            page_ahead = page_of(i + R::S * W);
+            issue(stage == 0 ? R::S - 1 : stage - 1);
             const bool ok = (there >> stage) & 1u;
             const uint32_t kb = ring + (uint32_t)(stage * R::STAGE), vb = kb + R::HALF;
             const float ks = sm_sc[warp][stage][0] * a.scale_log2, vs = sm_sc[warp][stage][1];
@@ -371,8 +405,8 @@ __global__ void __launch_bounds__(W * 32, D == 256 || NT == 2 ? 1 : 2) kv8_decod
             uint32_t pf[NT][2];
             if (ok) {
                 const float wv = vs > 0.0f ? vs : kTiny;
-                const float lw = log2f(wv), iw = 1.0f / wv;
-                const bool in0 = tok + g < len, in1 = tok + g + 8 < len;
+                const float lw = lg2(wv), iw = rcp(wv);
+                const bool in0 = g < left, in1 = g + 8 < left;
                 float y[NT][4];
                 bool move = false;
 #pragma unroll
@@ -434,150 +468,112 @@ __global__ void __launch_bounds__(W * 32, D == 256 || NT == 2 ? 1 : 2) kv8_decod
                 }
             }
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        if (bad && lane == 0) atomicExch(a.status, (int)W4A8_ERR_PAGE);
 
-        // merge the warps: M = max m_w, O = sum 2^(m_w - M) O_w, L likewise (warp order)
+        // the segment's end: l over the lanes, then out, or this part to the workspace
+        const bool whole = get.first == 0 && get.last == get.nt;
+        const size_t slot = 2 * (size_t)c + (get.ub + (long long)get.head * get.nt + get.first == u0 ? 0 : 1);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], d);
-                if (g == 0) {
-                    sm_m[warp][8 * n + 2 * t + e] = m[n][e];
-                    sm_l[warp][8 * n + 2 * t + e] = l[n][e];
-                }
-            }
-        __syncthreads();                              // also: every warp is done with its ring
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
                 const int h = 8 * n + 2 * t + e;
-                float M = -INFINITY;
+                if (h < a.G) {
+                    const float inv = l[n][e] > 0.0f ? 1.0f / l[n][e] : 0.0f;
+                    // a lane holds runs of consecutive d: 8 (D = 64) or 16
 #pragma unroll
-                for (int w = 0; w < W; ++w) M = fmaxf(M, sm_m[w][h]);
-                const float f = m[n][e] == -INFINITY ? 0.0f : ex2(m[n][e] - M);
+                    for (int j = 0; j < NJ; j += 4) {
+                        const int d0 = row_dim<D>(j, 0, g);
+                        if (whole) {
+                            uint32_t w[4];
 #pragma unroll
-                for (int j = 0; j < NJ; ++j) {
-                    o[n][j][e] *= f;
-                    o[n][j][e + 2] *= f;
-                }
-            }
-        // the upper half of the warps hand theirs to the lower half
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            if (warp / (W / 2) == 1 - half) {
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float *at = sm_o + ((size_t)(warp % (W / 2)) * NH + 8 * n + 2 * t + e) * D;
-#pragma unroll
-                        for (int j = 0; j < NJ; ++j) {
-                            if (half) {
-                                at[row_dim<D>(j, 0, g)] += o[n][j][e];
-                                at[row_dim<D>(j, 1, g)] += o[n][j][e + 2];
-                            } else {
-                                at[row_dim<D>(j, 0, g)] = o[n][j][e];
-                                at[row_dim<D>(j, 1, g)] = o[n][j][e + 2];
+                            for (int k = 0; k < 4; ++k) {
+                                const __half2 v = __floats2half2_rn(o[n][j + k][e] * inv, o[n][j + k][e + 2] * inv);
+                                w[k] = *reinterpret_cast<const uint32_t *>(&v);
                             }
+                            *reinterpret_cast<uint4 *>(a.out + (row0 + h) * D + d0) = make_uint4(w[0], w[1], w[2], w[3]);
+                        } else {
+                            float *to = a.ws_o + (slot * a.G + h) * D + d0;
+                            *reinterpret_cast<float4 *>(to) = make_float4(o[n][j][e], o[n][j][e + 2], o[n][j + 1][e], o[n][j + 1][e + 2]);
+                            *reinterpret_cast<float4 *>(to + 4) = make_float4(o[n][j + 2][e], o[n][j + 2][e + 2], o[n][j + 3][e], o[n][j + 3][e + 2]);
                         }
                     }
-            }
-            __syncthreads();
-        }
-        const bool whole = first == 0 && last == nt;
-        const int slot = 2 * (int)c + (u == u0 ? 0 : 1);
-        for (int i = threadIdx.x; i < a.G * D; i += W * 32) {
-            const int h = i / D;
-            float v = 0.0f;
-#pragma unroll
-            for (int w = 0; w < W / 2; ++w) v += sm_o[(size_t)w * NH * D + i];
-            float M = -INFINITY, L = 0.0f;
-#pragma unroll
-            for (int w = 0; w < W; ++w) M = fmaxf(M, sm_m[w][h]);
-#pragma unroll
-            for (int w = 0; w < W; ++w)
-                if (sm_m[w][h] != -INFINITY) L = fmaf(sm_l[w][h], ex2(sm_m[w][h] - M), L);
-            if (whole) {
-                const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-                a.out[((size_t)b * a.Hkv + head) * (size_t)a.G * D + i] = __half_as_ushort(__float2half_rn(v * inv));
-            } else {
-                a.ws_o[(size_t)slot * a.G * D + i] = v;
-                if (i % D == 0) {
-                    a.ws_ml[((size_t)slot * a.G + h) * 2] = M;
-                    a.ws_ml[((size_t)slot * a.G + h) * 2 + 1] = L;
+                    if (!whole && g == 0) {
+                        a.ws_ml[(slot * a.G + h) * 2] = m[n][e];
+                        a.ws_ml[(slot * a.G + h) * 2 + 1] = l[n][e];
+                    }
                 }
             }
+        if (get.first == 0 && lane == 0) {
+            const long long us = get.ub + (long long)get.head * get.nt;
+            const int n = whole ? 1 : kv8::worker_of_unit(us + get.nt - 1, U, C) - (int)c + 1;
+            a.ws_parts[(size_t)get.b * a.Hkv + get.head] = make_int2((int)slot, n);
         }
-        __syncthreads();
-        u = us + last;
+        if (!next_segment(a, get, u1)) break;
     }
+    if (bad && lane == 0) atomicExch(a.status, (int)W4A8_ERR_PAGE);
+    asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// One CTA per (query head, sequence): nothing where the pair was one CTA's
+// One CTA per (query head, sequence): nothing where the pair was one warp's
 // whole segment, zeros for an empty sequence, else the parts' merge
 //   M = max m_s,  out = sum_s o_s 2^(m_s - M) / sum_s l_s 2^(m_s - M),
 // the parts spread over groups of D / 4 threads and folded in a fixed order.
-constexpr int NC = 512;
+constexpr int NC = 1024;             // threads at most
 
-__global__ void __launch_bounds__(NC) kv8_combine_kernel(const DecodeArgs a, int D, long long grid) {
-    __shared__ float sm_w[MAXC];
+__global__ void __launch_bounds__(NC) kv8_combine_kernel(const DecodeArgs a, int D) {
+    __shared__ float sm_w[MAXW];
     __shared__ float4 sm_p[NC];
     __shared__ float sm_r[2][NC / 32];
-    __shared__ long long sm_scan[32];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int hq = blockIdx.x, b = blockIdx.y;
+    const int hq = blockIdx.x, b = blockIdx.y, nt = blockDim.x;
     const int head = hq / a.G, h = hq - head * a.G;
     const size_t out_at = ((size_t)b * a.Hkv * a.G + hq) * D;
-    const int nt = seq_tiles(a, b);
-    if (nt == 0) {
-        for (int i = threadIdx.x; i < D; i += NC) a.out[out_at + i] = 0;
+    // (the pair's entry is written only where the sequence has tokens)
+    const int len = seq_len(a, b);
+    const int2 parts = a.ws_parts[(size_t)b * a.Hkv + head];
+    if (len == 0) {
+        for (int i = threadIdx.x; i < D; i += nt) a.out[out_at + i] = 0;
         return;
     }
-    long long mine = 0, skip, lead = 0;
-    for (int i = threadIdx.x; i < a.B; i += NC) {
-        const int n = seq_tiles(a, i);
-        mine += n;
-        if (i < b) lead += n;
-    }
-    const long long U = block_scan(mine, sm_scan, skip) * a.Hkv, C = min(grid, U);
-    lead = block_scan(lead, sm_scan, skip);
-    const long long us = lead * a.Hkv + (long long)head * nt;
-    const int c0 = kv8::worker_of_unit(us, U, C), c1 = kv8::worker_of_unit(us + nt - 1, U, C);
-    if (c0 == c1) return;
-    const int n = c1 - c0 + 1;
-    // part p is CTA c0 + p's; its slot is 0 where the CTA's first unit is the pair's
-    auto slot = [&](int p) { return 2 * (c0 + p) + (p == 0 && kv8::first_unit(c0, U, C) < us ? 1 : 0); };
+    const int n = parts.y;
+    if (n <= 1) return;
+    // the first part is in the slot that its worker named, the others in their workers' first
+    auto slot = [&](int p) { return p == 0 ? parts.x : (parts.x & ~1) + 2 * p; };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    float M = -INFINITY;
-    for (int p = threadIdx.x; p < n; p += NC) M = fmaxf(M, a.ws_ml[((size_t)slot(p) * a.G + h) * 2]);
+    float M = -INFINITY, m0 = 0.0f, l0 = 0.0f;               // (the first pair is kept: one round trip for up to nt parts)
+    for (int p = threadIdx.x; p < n; p += nt) {
+        const float2 ml = *reinterpret_cast<const float2 *>(a.ws_ml + ((size_t)slot(p) * a.G + h) * 2);
+        if (p < nt) {
+            m0 = ml.x;
+            l0 = ml.y;
+        }
+        M = fmaxf(M, ml.x);
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     if (lane == 0) sm_r[0][warp] = M;
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < NC / 32; ++w) M = fmaxf(M, sm_r[0][w]);
+    for (int w = 0; w < nt / 32; ++w) M = fmaxf(M, sm_r[0][w]);
     float L = 0.0f;
-    for (int p = threadIdx.x; p < n; p += NC) {
-        const float *ml = a.ws_ml + ((size_t)slot(p) * a.G + h) * 2;
-        const float w = ml[0] == -INFINITY ? 0.0f : ex2(ml[0] - M);
+    for (int p = threadIdx.x; p < n; p += nt) {
+        float2 ml = make_float2(m0, l0);
+        if (p >= nt) ml = *reinterpret_cast<const float2 *>(a.ws_ml + ((size_t)slot(p) * a.G + h) * 2);
+        const float w = ml.x == -INFINITY ? 0.0f : ex2(ml.x - M);
         sm_w[p] = w;
-        L = fmaf(ml[1], w, L);
+        L = fmaf(ml.y, w, L);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
     if (lane == 0) sm_r[1][warp] = L;
     __syncthreads();
     L = 0.0f;
-#pragma unroll
-    for (int w = 0; w < NC / 32; ++w) L += sm_r[1][w];
-    const int per = D / 4, groups = NC / per, grp = threadIdx.x / per, col = (threadIdx.x % per) * 4;
+    for (int w = 0; w < nt / 32; ++w) L += sm_r[1][w];
+    const int per = D / 4, groups = nt / per, grp = threadIdx.x / per, col = (threadIdx.x % per) * 4;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
     for (int p = grp; p < n; p += groups) {
         const float4 v = *reinterpret_cast<const float4 *>(a.ws_o + ((size_t)slot(p) * a.G + h) * D + col);
         const float w = sm_w[p];
@@ -617,7 +613,6 @@ template <int D, int NT>
 w4a8_status launch_decode(const DecodeArgs &a, int C, cudaStream_t stream) {
     static std::atomic<int> attr_done[w4a8_host::kDeviceSlots];
     const int smem = Ring<D>::BYTES;
-    static_assert(Ring<D>::BYTES >= W / 2 * 8 * NT * D * 4, "O of half the warps in the rings' space");
     const w4a8_status st = w4a8_host::ensure_smem_limit(kv8_decode_kernel<D, NT>, smem, attr_done);
     if (st != W4A8_OK) return st;
     return w4a8_host::launch_dependent(kv8_decode_kernel<D, NT>, dim3((unsigned)C), W * 32, (size_t)smem, stream, a);
@@ -630,23 +625,50 @@ size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 namespace w4a8_host {
 
 size_t kv8_decode_workspace_bytes(int B, int Hq, int Hkv, int D, int T, int maxp) {
-    const size_t rows = (size_t)2 * split_ctas(B, Hq, Hkv, D, T, maxp) * (Hq / Hkv);
-    return align256(rows * D * 4) + rows * 2 * 4;
+    const size_t rows = (size_t)2 * W * split_ctas(B, Hq, Hkv, D, T, maxp) * (Hq / Hkv);
+    return align256(rows * D * 4) + align256(rows * 2 * 4) + (size_t)B * Hkv * sizeof(int2);
 }
 
 w4a8_status launch_kv8_decode(const uint16_t *q, const Kv8Cache &c, const int32_t *table, const int32_t *lens, int B,
                               int Hq, int maxp, float scale, uint16_t *out, void *workspace, cudaStream_t stream) {
     const int C = split_ctas(B, Hq, c.Hkv, c.D, c.T, maxp), G = Hq / c.Hkv;
-    DecodeArgs a = {q, c.k_codes, c.v_codes, c.k_scale, c.v_scale, table, lens, out, static_cast<float *>(workspace),
-                    reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + align256((size_t)2 * C * G * c.D * 4)),
-                    c.P, c.Hkv, c.T, B, maxp, G, scale * 1.4426950408889634f, device_status_ptr()};
+    const size_t rows = (size_t)2 * W * C * G;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    DecodeArgs a = {};
+    a.q = q;
+    a.kc = c.k_codes;
+    a.vc = c.v_codes;
+    a.ks = c.k_scale;
+    a.vs = c.v_scale;
+    a.table = table;
+    a.lens = lens;
+    a.out = out;
+    a.ws_o = reinterpret_cast<float *>(ws);
+    a.ws_ml = reinterpret_cast<float *>(ws + align256(rows * c.D * 4));
+    a.ws_parts = reinterpret_cast<int2 *>(ws + align256(rows * c.D * 4) + align256(rows * 2 * 4));
+    a.P = c.P;
+    a.Hkv = c.Hkv;
+    a.T = c.T;
+    a.T_log2 = c.T == 16 ? 4 : c.T == 32 ? 5 : c.T == 64 ? 6 : 7;
+    a.B = B;
+    a.maxp = maxp;
+    a.G = G;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.status = device_status_ptr();
     if (!a.status) return W4A8_ERR_CUDA;
     w4a8_status st = W4A8_ERR_UNSUPPORTED;
     if (c.D == 64) st = G <= 8 ? launch_decode<64, 1>(a, C, stream) : launch_decode<64, 2>(a, C, stream);
     if (c.D == 128) st = G <= 8 ? launch_decode<128, 1>(a, C, stream) : launch_decode<128, 2>(a, C, stream);
     if (c.D == 256) st = G <= 8 ? launch_decode<256, 1>(a, C, stream) : launch_decode<256, 2>(a, C, stream);
     if (st != W4A8_OK) return st;
-    return launch_dependent(kv8_combine_kernel, dim3((unsigned)Hq, (unsigned)B), NC, 0, stream, a, c.D, (long long)C);
+    // threads: groups of D / 4 for about 4 parts each (there are W C parts for
+    // B Hkv pairs, up to a part for each 64 tokens)
+    long long parts = (long long)W * C / ((long long)B * c.Hkv) + 1;
+    const long long tiles = ((long long)maxp * c.T + TILE - 1) / TILE;
+    if (parts > tiles) parts = tiles;
+    int threads = c.D / 4 < 64 ? 64 : c.D / 4;
+    while (threads < NC && threads / (c.D / 4) * 4 < parts) threads *= 2;
+    return launch_dependent(kv8_combine_kernel, dim3((unsigned)Hq, (unsigned)B), threads, 0, stream, a, c.D);
 }
 
 }  // namespace w4a8_host
