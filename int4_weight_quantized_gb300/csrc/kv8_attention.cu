@@ -516,10 +516,13 @@ __global__ void __launch_bounds__(W * 32, D == 256 || NT == 2 ? 1 : 2) kv8_decod
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// One CTA per (query head, sequence): nothing where the pair was one warp's
-// whole segment, zeros for an empty sequence, else the parts' merge
+// One CTA per (query head, sequence) and share of d: nothing where the pair was
+// one warp's whole segment, zeros for an empty sequence, else the parts' merge
 //   M = max m_s,  out = sum_s o_s 2^(m_s - M) / sum_s l_s 2^(m_s - M),
-// the parts spread over groups of D / 4 threads and folded in a fixed order.
+// the parts spread over groups of threads that hold the share of d, and folded
+// in a fixed order.  Few pairs have many parts each (one sequence of 131072
+// tokens: 1216), and one SM reads them at its own rate: the shares of d spread
+// them over four times as many.
 constexpr int NC = 1024;             // threads at most
 
 __global__ void __launch_bounds__(NC) kv8_combine_kernel(const DecodeArgs a, int D) {
@@ -528,14 +531,14 @@ __global__ void __launch_bounds__(NC) kv8_combine_kernel(const DecodeArgs a, int
     __shared__ float sm_r[2][NC / 32];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int hq = blockIdx.x, b = blockIdx.y, nt = blockDim.x;
+    const int hq = blockIdx.x, b = blockIdx.y, nt = blockDim.x, Dz = D / (int)gridDim.z, d0 = (int)blockIdx.z * Dz;
     const int head = hq / a.G, h = hq - head * a.G;
-    const size_t out_at = ((size_t)b * a.Hkv * a.G + hq) * D;
+    const size_t out_at = ((size_t)b * a.Hkv * a.G + hq) * D + d0;
     // (the pair's entry is written only where the sequence has tokens)
     const int len = seq_len(a, b);
     const int2 parts = a.ws_parts[(size_t)b * a.Hkv + head];
     if (len == 0) {
-        for (int i = threadIdx.x; i < D; i += nt) a.out[out_at + i] = 0;
+        for (int i = threadIdx.x; i < Dz; i += nt) a.out[out_at + i] = 0;
         return;
     }
     const int n = parts.y;
@@ -571,27 +574,30 @@ __global__ void __launch_bounds__(NC) kv8_combine_kernel(const DecodeArgs a, int
     __syncthreads();
     L = 0.0f;
     for (int w = 0; w < nt / 32; ++w) L += sm_r[1][w];
-    const int per = D / 4, groups = nt / per, grp = threadIdx.x / per, col = (threadIdx.x % per) * 4;
+    const int per = Dz / 4, groups = nt / per, grp = threadIdx.x / per, col = (threadIdx.x % per) * 4;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
     for (int p = grp; p < n; p += groups) {
-        const float4 v = *reinterpret_cast<const float4 *>(a.ws_o + ((size_t)slot(p) * a.G + h) * D + col);
+        const float4 v = *reinterpret_cast<const float4 *>(a.ws_o + ((size_t)slot(p) * a.G + h) * D + d0 + col);
         const float w = sm_w[p];
         s.x = fmaf(v.x, w, s.x);
         s.y = fmaf(v.y, w, s.y);
         s.z = fmaf(v.z, w, s.z);
         s.w = fmaf(v.w, w, s.w);
     }
-    sm_p[threadIdx.x] = s;
-    __syncthreads();
-    if (grp == 0) {
-        for (int k = 1; k < groups; ++k) {
-            const float4 v = sm_p[k * per + threadIdx.x];
+    for (int half = groups / 2; half > 0; half /= 2) {       // groups is a power of two
+        if (grp >= half && grp < 2 * half) sm_p[threadIdx.x - half * per] = s;
+        __syncthreads();
+        if (grp < half) {
+            const float4 v = sm_p[threadIdx.x];
             s.x += v.x;
             s.y += v.y;
             s.z += v.z;
             s.w += v.w;
         }
+        __syncthreads();
+    }
+    if (grp == 0) {
         const float inv = L > 0.0f ? 1.0f / L : 0.0f;
         const __half2 lo = __floats2half2_rn(s.x * inv, s.y * inv), hi = __floats2half2_rn(s.z * inv, s.w * inv);
         uint2 pk;
@@ -661,14 +667,16 @@ w4a8_status launch_kv8_decode(const uint16_t *q, const Kv8Cache &c, const int32_
     if (c.D == 128) st = G <= 8 ? launch_decode<128, 1>(a, C, stream) : launch_decode<128, 2>(a, C, stream);
     if (c.D == 256) st = G <= 8 ? launch_decode<256, 1>(a, C, stream) : launch_decode<256, 2>(a, C, stream);
     if (st != W4A8_OK) return st;
-    // threads: groups of D / 4 for about 4 parts each (there are W C parts for
-    // B Hkv pairs, up to a part for each 64 tokens)
+    // threads: a group (a share of d) for about 4 parts (there are W C parts for
+    // B Hkv pairs, up to a part for each 64 tokens); four shares of d where a
+    // pair has more parts than the threads of one CTA take at once
     long long parts = (long long)W * C / ((long long)B * c.Hkv) + 1;
     const long long tiles = ((long long)maxp * c.T + TILE - 1) / TILE;
     if (parts > tiles) parts = tiles;
-    int threads = c.D / 4 < 64 ? 64 : c.D / 4;
-    while (threads < NC && threads / (c.D / 4) * 4 < parts) threads *= 2;
-    return launch_dependent(kv8_combine_kernel, dim3((unsigned)Hq, (unsigned)B), threads, 0, stream, a, c.D);
+    const int z = parts > NC / (c.D / 4) * 4 ? 4 : 1, per = c.D / 4 / z;
+    int threads = per < 64 ? 64 : per;
+    while (threads < NC && threads / per * 4 < parts) threads *= 2;
+    return launch_dependent(kv8_combine_kernel, dim3((unsigned)Hq, (unsigned)B, (unsigned)z), threads, 0, stream, a, c.D);
 }
 
 }  // namespace w4a8_host

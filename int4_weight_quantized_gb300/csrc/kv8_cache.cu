@@ -26,6 +26,33 @@ using namespace w4a8;
 
 constexpr int WARPS = 4;
 
+// Eight codes clamp(rint(fl(x / s))), by the reciprocal r = fl(1 / s) where that
+// is certain: t = fl(x r) and the quotient fl(x / s) are both within 2^-23
+// (relative) of x / s, |x / s| <= 127 (1 + 2^-23), so they differ by less than
+// 2.3e-5 < 2^-15; where t is 2^-14 or more from every half-integer, no rounding
+// border lies between them.  The others (and whatever is not finite) are
+// divided.  1.5 * 2^23 added to t leaves rint(t) in the low bits.
+__device__ __forceinline__ uint2 codes8(uint4 x, float s, float r) {
+    const __half2 *h = reinterpret_cast<const __half2 *>(&x);
+    uint32_t q[8];
+    unsigned near = 0u;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float f = e & 1 ? __high2float(h[e / 2]) : __low2float(h[e / 2]);
+        const float t = f * r, m = t + kMagic;
+        if (!(fabsf(t - (m - kMagic)) <= 0.5f - 0x1p-14f)) near |= 1u << e;
+        q[e] = __float_as_uint(m);
+    }
+    if (near) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (near & (1u << e)) q[e] = (uint32_t)act_code(e & 1 ? __high2float(h[e / 2]) : __low2float(h[e / 2]), s);
+    }
+    const uint32_t a = __byte_perm(q[0], q[1], 0x0040), b = __byte_perm(q[2], q[3], 0x0040);
+    const uint32_t c = __byte_perm(q[4], q[5], 0x0040), d = __byte_perm(q[6], q[7], 0x0040);
+    return make_uint2(__byte_perm(a, b, 0x5410), __byte_perm(c, d, 0x5410));
+}
+
 struct AppendArgs {
     const uint16_t *x[2];      // K, V rows
     long long ld[2];           // elements between tokens
@@ -78,19 +105,18 @@ __global__ void __launch_bounds__(WARPS * 32) kv8_append_kernel(const AppendArgs
     float *sp = (kv ? a.scale[1] : a.scale[0]) + kv8::scale_offset(page, a.Hkv, head, a.T, tok0 % a.T);
     int8_t *cp = (kv ? a.codes[1] : a.codes[0]) + kv8::code_offset(page, a.Hkv, head, a.T, tok0 % a.T, D) + col;
     const float s_old = lo > 0 ? *sp : 0.0f;
-    float amax = 0.0f;
+    __half2 top = __halves2half2(__ushort_as_half(0), __ushort_as_half(0));
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
         const __half2 *h = reinterpret_cast<const __half2 *>(&v[i]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float2 f = __half22float2(h[e]);
-            amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-        }
+        for (int e = 0; e < 4; ++e) top = __hmax2(top, __habs2(h[e]));
     }
+    float amax = fmaxf(__low2float(top), __high2float(top));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     const float s = fmaxf(s_old, __fdiv_rn(amax, 127.0f));
+    const float recip = __fdiv_rn(1.0f, s);
     const bool again = lo > 0 && s > s_old;        // earlier codes of the block change
     const float f_old = again ? __fdiv_rn(s_old, s) : 1.0f;
 #pragma unroll
@@ -98,15 +124,7 @@ __global__ void __launch_bounds__(WARPS * 32) kv8_append_kernel(const AppendArgs
         const int t = i * RPP + row;
         uint32_t *dst = reinterpret_cast<uint32_t *>(cp + (size_t)t * D);
         if (t >= lo && t < hi) {
-            const __half2 *h = reinterpret_cast<const __half2 *>(&v[i]);
-            int q[8];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 f = __half22float2(h[e]);
-                q[2 * e] = s > 0.0f ? act_code(f.x, s) : 0;
-                q[2 * e + 1] = s > 0.0f ? act_code(f.y, s) : 0;
-            }
-            *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bytes4(q[0], q[1], q[2], q[3]), pack_bytes4(q[4], q[5], q[6], q[7]));
+            *reinterpret_cast<uint2 *>(dst) = s > 0.0f ? codes8(v[i], s, recip) : make_uint2(0u, 0u);
         } else if (t < lo && again) {
             const uint2 w = *reinterpret_cast<const uint2 *>(dst);
             uint32_t u[2] = {w.x, w.y};
@@ -172,8 +190,11 @@ __global__ void __launch_bounds__(WARPS * 32) kv8_read_kernel(const ReadArgs a) 
             uint32_t o[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const uint32_t u = w[e / 2] >> (16 * (e & 1));
-                const __half2 h = __floats2half2_rn((float)(int8_t)u * s, (float)(int8_t)(u >> 8) * s);
+                // code + 128 in the mantissa of 2^23, less 2^23 + 128: exact
+                const uint32_t u = w[e / 2] ^ 0x80808080u;
+                const float a0 = __uint_as_float(__byte_perm(u, 0x4B000000u, e & 1 ? 0x7442 : 0x7440)) - 8388736.0f;
+                const float a1 = __uint_as_float(__byte_perm(u, 0x4B000000u, e & 1 ? 0x7443 : 0x7441)) - 8388736.0f;
+                const __half2 h = __floats2half2_rn(a0 * s, a1 * s);
                 o[e] = *reinterpret_cast<const uint32_t *>(&h);
             }
             uint4 *dst = reinterpret_cast<uint4 *>(out + (size_t)t * a.Hkv * D);

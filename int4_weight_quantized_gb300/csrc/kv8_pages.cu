@@ -56,7 +56,8 @@ __device__ __forceinline__ int scan_block(int v, int *sm, int &before) {
     return total;
 }
 
-// Sum over the cluster's CTAs of their block totals: (all, those of lower rank).
+// Sum over the cluster's CTAs of their block totals: (all, those of lower
+// rank).  Each use has its own word *sm, which peers may read until the end.
 __device__ __forceinline__ int scan_cluster(int mine, int *sm, int rank, int &before) {
     if (threadIdx.x == 0) *sm = mine;
     cluster_sync_all();
@@ -68,7 +69,6 @@ __device__ __forceinline__ int scan_cluster(int mine, int *sm, int rank, int &be
         if (r < rank) before += v;
         all += v;
     }
-    cluster_sync_all();                          // nobody overwrites *sm before all have read it
     return all;
 }
 
@@ -77,26 +77,42 @@ __device__ __forceinline__ uint32_t bits_below(long long n) { return n <= 0 ? 0u
 __global__ void __launch_bounds__(NT) __cluster_dims__(CL, 1, 1) kv8_mark_kernel(const MarkArgs a) {
     extern __shared__ uint32_t map[];            // this CTA's words of the bitmap
     __shared__ int sm_w[NT / 32];
-    __shared__ int sm_c;
+    __shared__ int sm_c[4];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int rank = blockIdx.x;
     for (int i = threadIdx.x; i < a.words; i += NT) map[i] = 0u;
-    cluster_sync_all();
     const uint32_t base = smem_u32(map);
-    const long long entries = (long long)a.S * a.maxp;
-    for (long long e = (long long)rank * NT + threadIdx.x; e < entries; e += (long long)CL * NT) {
-        const int b = (int)(e / a.maxp), i = (int)(e - (long long)b * a.maxp);
-        const int len = a.lens[b];
-        if (len <= 0 || i > (len - 1) / a.T) continue;
-        const int id = a.table[e];
-        if (id < 0 || id >= a.P) {
-            atomicExch(a.status, (int)W4A8_ERR_PAGE);
-            continue;
+    const long long entries = (long long)a.S * a.maxp, step = (long long)CL * NT;
+    bool cleared = false;
+    // four entries at a time, their lengths and pages all on the way together
+    // (entries that do not count are read too: the table has them)
+    for (long long e0 = 0; e0 < entries || !cleared; e0 += 4 * step) {
+        int id[4], len[4], at[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const long long e = e0 + k * step + (long long)rank * NT + threadIdx.x;
+            id[k] = len[k] = at[k] = 0;
+            if (e < entries) {
+                const int b = (int)(e / a.maxp);
+                at[k] = (int)(e - (long long)b * a.maxp);
+                len[k] = a.lens[b];
+                id[k] = a.table[e];
+            }
         }
-        const int w = id >> 5, owner = w / a.words;
-        const uint32_t at = dsmem_addr(base + (uint32_t)(w - owner * a.words) * 4u, (uint32_t)owner);
-        asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(at), "r"(1u << (id & 31)) : "memory");
+        if (!cleared) cluster_sync_all();        // every CTA's map is clear
+        cleared = true;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (len[k] <= 0 || at[k] > (len[k] - 1) / a.T) continue;
+            if (id[k] < 0 || id[k] >= a.P) {
+                atomicExch(a.status, (int)W4A8_ERR_PAGE);
+                continue;
+            }
+            const int w = id[k] >> 5, owner = w / a.words;
+            const uint32_t to = dsmem_addr(base + (uint32_t)(w - owner * a.words) * 4u, (uint32_t)owner);
+            asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(to), "r"(1u << (id[k] & 31)) : "memory");
+        }
     }
     cluster_sync_all();
 
@@ -108,19 +124,20 @@ __global__ void __launch_bounds__(NT) __cluster_dims__(CL, 1, 1) kv8_mark_kernel
     int held = 0, before;
     for (int w = w0; w < w1; ++w) held += __popc(map[w]);
     int skip, tot = scan_block(held, sm_w, before);
-    const int n = scan_cluster(tot, &sm_c, rank, skip);          // held pages
+    const int n = scan_cluster(tot, &sm_c[0], rank, skip);          // held pages
 
     if (a.ids) {
         const int nfree = a.P - n;
         int there = 0;
         for (int w = w0; w < w1; ++w) there += __popc(~map[w] & pages(w));
         tot = scan_block(there, sm_w, before);
-        scan_cluster(tot, &sm_c, rank, skip);
+        scan_cluster(tot, &sm_c[1], rank, skip);
         int at = skip + before;
         for (int w = w0; w < w1; ++w)
             for (uint32_t m = ~map[w] & pages(w); m; m &= m - 1) a.ids[at++] = (int)(first + (long long)w * 32) + __ffs(m) - 1;
         for (long long i = nfree + (long long)rank * NT + threadIdx.x; i < a.P; i += CL * NT) a.ids[i] = -1;
         if (rank == 0 && threadIdx.x == 0) *a.count = nfree;
+        cluster_sync_all();                      // no CTA leaves while a peer may still read its words
         return;
     }
     // holes: free pages below n; movers: held pages from n on; as many of each
@@ -129,14 +146,14 @@ __global__ void __launch_bounds__(NT) __cluster_dims__(CL, 1, 1) kv8_mark_kernel
     int c = 0;
     for (int w = w0; w < w1; ++w) c += __popc(hole_bits(w));
     tot = scan_block(c, sm_w, before);
-    scan_cluster(tot, &sm_c, rank, skip);
+    scan_cluster(tot, &sm_c[1], rank, skip);
     int at = skip + before;
     for (int w = w0; w < w1; ++w)
         for (uint32_t m = hole_bits(w); m; m &= m - 1) a.holes[at++] = (int)(first + (long long)w * 32) + __ffs(m) - 1;
     c = 0;
     for (int w = w0; w < w1; ++w) c += __popc(mover_bits(w));
     tot = scan_block(c, sm_w, before);
-    const int moves = scan_cluster(tot, &sm_c, rank, skip);      // its barriers also order the holes' list
+    const int moves = scan_cluster(tot, &sm_c[2], rank, skip);      // its barriers also order the holes' list
     at = skip + before;
     for (int w = w0; w < w1; ++w)
         for (uint32_t m = mover_bits(w); m; m &= m - 1, ++at) {
@@ -148,6 +165,7 @@ __global__ void __launch_bounds__(NT) __cluster_dims__(CL, 1, 1) kv8_mark_kernel
         *a.count = n;
         *a.moves = moves;
     }
+    cluster_sync_all();
 }
 
 // ------------------------------------------------------------ page contents
@@ -204,10 +222,35 @@ struct CompactArgs {
     int S, maxp, T, P;
 };
 
-__global__ void __launch_bounds__(CT) kv8_compact_kernel(const CompactArgs a) {
+__global__ void __launch_bounds__(CT, 6) kv8_compact_kernel(const CompactArgs a) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int n = *a.count, moves = *a.moves;
+    const int chunks = copy_chunks(a.copy.code_bytes);
+    const long long work = (long long)moves * chunks;
+    // a page's chunks go to CTAs side by side; the next chunk's pages are looked
+    // up while this one is copied
+    int m = (int)(blockIdx.x / (unsigned)chunks), part = (int)(blockIdx.x % (unsigned)chunks);
+    const int dm = (int)(gridDim.x / (unsigned)chunks), dp = (int)(gridDim.x % (unsigned)chunks);
+    int src = 0, dst = 0;
+    if (blockIdx.x < work) {
+        src = a.movers[m];
+        dst = a.holes[m];
+    }
+    for (long long w = blockIdx.x; w < work; w += gridDim.x) {
+        const int s0 = src, d0 = dst, p0 = part;
+        m += dm;
+        part += dp;
+        if (part >= chunks) {
+            part -= chunks;
+            ++m;
+        }
+        if (w + gridDim.x < work) {
+            src = a.movers[m];
+            dst = a.holes[m];
+        }
+        copy_part(a.copy, s0, d0, p0);
+    }
     const long long entries = (long long)a.S * a.maxp;
     for (long long e = (long long)blockIdx.x * CT + threadIdx.x; e < entries; e += (long long)gridDim.x * CT) {
         const int b = (int)(e / a.maxp), i = (int)(e - (long long)b * a.maxp);
@@ -219,12 +262,6 @@ __global__ void __launch_bounds__(CT) kv8_compact_kernel(const CompactArgs a) {
             else if (id >= n) id = a.remap[id];
         }
         a.table_out[e] = id;
-    }
-    const int chunks = copy_chunks(a.copy.code_bytes);
-    const long long work = (long long)moves * chunks;
-    for (long long w = blockIdx.x; w < work; w += gridDim.x) {
-        const int m = (int)(w / chunks);
-        copy_part(a.copy, a.movers[m], a.holes[m], (int)(w - (long long)m * chunks));
     }
 }
 
