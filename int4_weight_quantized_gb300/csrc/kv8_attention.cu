@@ -16,10 +16,11 @@
 //
 // Tiles.  A warp takes 16 tokens (one scale block) at a time.  Its own ring of
 // asynchronous copies in shared memory keeps the next blocks' K, V and scales
-// in flight while it works on one: no warp waits for another, and 96 KB or
-// more per SM are on the way, three times what the memory's latency needs at
-// its full rate (registers as the destination, 32 KB per SM, gave 228 us
-// where the ring gives RINGTIME on 682 MB).  The 16 tokens are the rows of
+// in flight while it works on one: 96 KB or more per SM are on the way, twice
+// what the memory's latency needs at its full rate (registers as the
+// destination, 32 KB per SM, gave 228 us where the ring gave 147, on 682 MB; a
+// range per CTA instead of per warp, its warps' sums merged at each segment's
+// end, left the SMs idle for a third of that: 116 us now, 5.9 TB/s).  The 16 tokens are the rows of
 // S^T = K Q^T, 16 values of d are the rows of O^T = V^T P^T (both mma.sync
 // m16n8k16), and 8 query heads are the columns of both, so a group of up to 8
 // heads wastes nothing that costs.  The order of d inside a product is free,
@@ -286,9 +287,12 @@ __global__ void __launch_bounds__(W * 32, D == 256 || NT == 2 ? 1 : 2) kv8_decod
     const long long U = block_scan(mine, sm_part, before) * a.Hkv;
     sm_scan[threadIdx.x] = before * a.Hkv;
     __syncthreads();
-    // this warp's range (no more workers than units: every worker of a pair
-    // then has a part of it); neighbours in the order are on different SMs
-    const long long C = min((long long)gridDim.x * W, U), c = (long long)warp * gridDim.x + blockIdx.x;
+    // this warp's range; neighbours in the order are on different SMs.  A worker
+    // for each unit up to 512 (a short step wants them all at once), then one
+    // for 4 units until every warp has work: parts cost a read and a write, and a
+    // ring is full with 3 blocks (one sequence of 131072 tokens: 36 us a call
+    // with a worker per unit, 29 so)
+    const long long C = min((long long)gridDim.x * W, max(min(U, 512LL), U / 4)), c = (long long)warp * gridDim.x + blockIdx.x;
     if (c >= C) return;
     const long long u0 = kv8::first_unit(c, U, C), u1 = kv8::first_unit(c + 1, U, C);
     Cursor put;                           // the block that is copied next
@@ -615,6 +619,13 @@ int split_ctas(int B, int Hq, int Hkv, int D, int T, int maxp) {
     return (int)(most < fit ? (most < 1 ? 1 : most) : fit);
 }
 
+// Workers that can have a part: a warp each, no more than there can be tiles.
+int split_workers(int B, int Hq, int Hkv, int D, int T, int maxp) {
+    const long long most = (long long)B * Hkv * (((long long)maxp * T + TILE - 1) / TILE);
+    const int warps = W * split_ctas(B, Hq, Hkv, D, T, maxp);
+    return most < warps ? (int)most : warps;
+}
+
 template <int D, int NT>
 w4a8_status launch_decode(const DecodeArgs &a, int C, cudaStream_t stream) {
     static std::atomic<int> attr_done[w4a8_host::kDeviceSlots];
@@ -631,14 +642,15 @@ size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 namespace w4a8_host {
 
 size_t kv8_decode_workspace_bytes(int B, int Hq, int Hkv, int D, int T, int maxp) {
-    const size_t rows = (size_t)2 * W * split_ctas(B, Hq, Hkv, D, T, maxp) * (Hq / Hkv);
+    const size_t rows = (size_t)2 * split_workers(B, Hq, Hkv, D, T, maxp) * (Hq / Hkv);
     return align256(rows * D * 4) + align256(rows * 2 * 4) + (size_t)B * Hkv * sizeof(int2);
 }
 
 w4a8_status launch_kv8_decode(const uint16_t *q, const Kv8Cache &c, const int32_t *table, const int32_t *lens, int B,
                               int Hq, int maxp, float scale, uint16_t *out, void *workspace, cudaStream_t stream) {
     const int C = split_ctas(B, Hq, c.Hkv, c.D, c.T, maxp), G = Hq / c.Hkv;
-    const size_t rows = (size_t)2 * W * C * G;
+    const int workers = split_workers(B, Hq, c.Hkv, c.D, c.T, maxp);
+    const size_t rows = (size_t)2 * workers * G;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     DecodeArgs a = {};
     a.q = q;
@@ -667,10 +679,10 @@ w4a8_status launch_kv8_decode(const uint16_t *q, const Kv8Cache &c, const int32_
     if (c.D == 128) st = G <= 8 ? launch_decode<128, 1>(a, C, stream) : launch_decode<128, 2>(a, C, stream);
     if (c.D == 256) st = G <= 8 ? launch_decode<256, 1>(a, C, stream) : launch_decode<256, 2>(a, C, stream);
     if (st != W4A8_OK) return st;
-    // threads: a group (a share of d) for about 4 parts (there are W C parts for
-    // B Hkv pairs, up to a part for each 64 tokens); four shares of d where a
-    // pair has more parts than the threads of one CTA take at once
-    long long parts = (long long)W * C / ((long long)B * c.Hkv) + 1;
+    // threads: a group (a share of d) for about 4 parts (a part for each worker
+    // of a pair, up to one for each 64 tokens); four shares of d where a pair has
+    // more parts than the threads of one CTA take at once
+    long long parts = workers / ((long long)B * c.Hkv) + 1;
     const long long tiles = ((long long)maxp * c.T + TILE - 1) / TILE;
     if (parts > tiles) parts = tiles;
     const int z = parts > NC / (c.D / 4) * 4 ? 4 : 1, per = c.D / 4 / z;

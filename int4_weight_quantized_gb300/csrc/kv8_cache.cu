@@ -64,7 +64,7 @@ struct AppendArgs {
 };
 
 template <int D>
-__global__ void __launch_bounds__(WARPS * 32) kv8_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(WARPS * 32, D == 64 ? 10 : D == 128 ? 8 : 5) kv8_append_kernel(const AppendArgs a) {
     constexpr int LPR = D / 8;              // lanes per row, 8 values each
     constexpr int RPP = 32 / LPR;           // rows per pass
     constexpr int NP = 16 / RPP;            // passes over the block's 16 rows

@@ -78,6 +78,7 @@ __global__ void __launch_bounds__(NT) __cluster_dims__(CL, 1, 1) kv8_mark_kernel
     extern __shared__ uint32_t map[];            // this CTA's words of the bitmap
     __shared__ int sm_w[NT / 32];
     __shared__ int sm_c[4];
+    __shared__ int sm_at[NT];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int rank = blockIdx.x;
@@ -116,56 +117,59 @@ __global__ void __launch_bounds__(NT) __cluster_dims__(CL, 1, 1) kv8_mark_kernel
     }
     cluster_sync_all();
 
-    // thread i takes the words [i per, (i + 1) per) of this CTA's
-    const int per = (a.words + NT - 1) / NT;
-    const int w0 = min(a.words, (int)threadIdx.x * per), w1 = min(a.words, w0 + per);
     const long long first = (long long)rank * a.words * 32;      // this CTA's first page
-    auto pages = [&](int w) { return bits_below((long long)a.P - (first + (long long)w * 32)); };   // real pages of a word
-    int held = 0, before;
-    for (int w = w0; w < w1; ++w) held += __popc(map[w]);
-    int skip, tot = scan_block(held, sm_w, before);
-    const int n = scan_cluster(tot, &sm_c[0], rank, skip);          // held pages
+    auto real = [&](int w) { return bits_below((long long)a.P - (first + (long long)w * 32)); };    // real pages of a word
+    // bits of this CTA's words, counted over the cluster
+    auto count = [&](auto bits, int *sm, int &skip) {
+        int c = 0, before;
+        for (int w = threadIdx.x; w < a.words; w += NT) c += __popc(bits(w));
+        const int mine = scan_block(c, sm_w, before);
+        return scan_cluster(mine, sm, rank, skip);
+    };
+    // act(rank of the page among the counted ones, page), a lane for each page
+    auto each = [&](auto bits, int skip, auto act) {
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        for (int w0 = 0; w0 < a.words; w0 += NT) {
+            const int w = w0 + threadIdx.x;
+            int before;
+            const int total = scan_block(w < a.words ? __popc(bits(w)) : 0, sm_w, before);
+            sm_at[threadIdx.x] = skip + before;
+            __syncthreads();
+            for (int i = warp; i < min(NT, a.words - w0); i += NT / 32) {
+                const uint32_t m = bits(w0 + i);
+                if (m >> lane & 1u) act(sm_at[i] + __popc(m & ((1u << lane) - 1u)), (int)(first + (long long)(w0 + i) * 32) + lane);
+            }
+            skip += total;
+            __syncthreads();
+        }
+    };
+    int skip;
+    const int n = count([&](int w) { return map[w]; }, &sm_c[0], skip);      // held pages
 
     if (a.ids) {
-        const int nfree = a.P - n;
-        int there = 0;
-        for (int w = w0; w < w1; ++w) there += __popc(~map[w] & pages(w));
-        tot = scan_block(there, sm_w, before);
-        scan_cluster(tot, &sm_c[1], rank, skip);
-        int at = skip + before;
-        for (int w = w0; w < w1; ++w)
-            for (uint32_t m = ~map[w] & pages(w); m; m &= m - 1) a.ids[at++] = (int)(first + (long long)w * 32) + __ffs(m) - 1;
+        auto free_bits = [&](int w) { return ~map[w] & real(w); };
+        const int nfree = count(free_bits, &sm_c[1], skip);
+        each(free_bits, skip, [&](int at, int id) { a.ids[at] = id; });
         for (long long i = nfree + (long long)rank * NT + threadIdx.x; i < a.P; i += CL * NT) a.ids[i] = -1;
         if (rank == 0 && threadIdx.x == 0) *a.count = nfree;
-        cluster_sync_all();                      // no CTA leaves while a peer may still read its words
-        return;
-    }
-    // holes: free pages below n; movers: held pages from n on; as many of each
-    auto hole_bits = [&](int w) { return ~map[w] & bits_below((long long)n - (first + (long long)w * 32)); };
-    auto mover_bits = [&](int w) { return map[w] & ~bits_below((long long)n - (first + (long long)w * 32)); };
-    int c = 0;
-    for (int w = w0; w < w1; ++w) c += __popc(hole_bits(w));
-    tot = scan_block(c, sm_w, before);
-    scan_cluster(tot, &sm_c[1], rank, skip);
-    int at = skip + before;
-    for (int w = w0; w < w1; ++w)
-        for (uint32_t m = hole_bits(w); m; m &= m - 1) a.holes[at++] = (int)(first + (long long)w * 32) + __ffs(m) - 1;
-    c = 0;
-    for (int w = w0; w < w1; ++w) c += __popc(mover_bits(w));
-    tot = scan_block(c, sm_w, before);
-    const int moves = scan_cluster(tot, &sm_c[2], rank, skip);      // its barriers also order the holes' list
-    at = skip + before;
-    for (int w = w0; w < w1; ++w)
-        for (uint32_t m = mover_bits(w); m; m &= m - 1, ++at) {
-            const int id = (int)(first + (long long)w * 32) + __ffs(m) - 1;
+    } else {
+        // holes: free pages below n; movers: held pages from n on; as many of each
+        auto below = [&](int w) { return bits_below((long long)n - (first + (long long)w * 32)); };
+        auto hole_bits = [&](int w) { return ~map[w] & below(w); };
+        auto mover_bits = [&](int w) { return map[w] & ~below(w); };
+        count(hole_bits, &sm_c[1], skip);
+        each(hole_bits, skip, [&](int at, int id) { a.holes[at] = id; });
+        const int moves = count(mover_bits, &sm_c[2], skip);     // its barrier also orders the holes' list
+        each(mover_bits, skip, [&](int at, int id) {
             a.movers[at] = id;
             a.remap[id] = a.holes[at];
+        });
+        if (rank == 0 && threadIdx.x == 0) {
+            *a.count = n;
+            *a.moves = moves;
         }
-    if (rank == 0 && threadIdx.x == 0) {
-        *a.count = n;
-        *a.moves = moves;
     }
-    cluster_sync_all();
+    cluster_sync_all();                          // no CTA leaves while a peer may still read its words
 }
 
 // ------------------------------------------------------------ page contents

@@ -28,10 +28,14 @@
 // the same p makes the choice of m exact), which after the first tiles is
 // rare.
 //
-// Neighbours.  A tile of keys may run into the next sequence.  Those scores
-// are masked by selection, and V's rows there never meet a product: the
-// product stops at the last group of 16 keys, whose rows past the end are
-// zeroed in shared memory (0 * inf would not be 0).
+// Masked places may hold anything.  Scores are masked by selection, so K never
+// reaches a row that does not see it; with V, 0 * inf would not be 0:
+//   - a tile of keys may run into the next sequence: the product stops at the
+//     last group of 16 keys, whose rows past the end are zeroed in shared memory;
+//   - on the diagonal some rows of a tile see a key and others do not: V's rows
+//     there are looked through, an inf or a NaN (which a working model has not)
+//     becomes zero and its key is noted, and the rows that do see the key get
+//     its value added at the end.
 #include <cuda.h>
 #include <math.h>
 
@@ -75,6 +79,8 @@ struct Cfg {
 
 struct PromptArgs {
     const int32_t *cu_q, *cu_k;
+    const uint16_t *v;
+    long long ld_v;
     uint16_t *out;
     int Tq, Tk, B, Hq, G, tok;       // tok: tokens per row tile, floor(128 / G)
     int causal;
@@ -193,7 +199,10 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     volatile uint32_t *tslot = reinterpret_cast<volatile uint32_t *>(empty + C::NSLOT);
     volatile uint32_t *abort_flag = tslot + 1;
 
+    __shared__ uint32_t sm_bad[4][4], sm_any;    // keys of the diagonal's tiles whose V is not finite
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x < 16) sm_bad[threadIdx.x >> 2][threadIdx.x & 3] = 0u;
+    if (threadIdx.x == 0) sm_any = 0u;
     constexpr int W_TMA = 4 * C::GROUPS, W_MMA = W_TMA + 1;
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::NQ; ++i) mbar_init(&qbar[i], 1);
@@ -436,13 +445,64 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         const int all_see = a.causal ? min(job.nk, job.t0 + grp * a.tok + off + 1) : job.nk;
         float m = -INFINITY, l = 0.0f;
         bool ok = true;
+        // V(j)'s tile of the ring, in the order of loading
+        auto v_tile = [&](int j) { return C::K_FIRST && j + 1 < nmax ? 2 * j + 2 : 2 * j + 1; };
+        // the first diagonal tile of the CTA's rows; they see the diagonal's keys in
+        // up to 3 tiles (at most 256 tokens)
+        const int diag0 = max(job.t0 + off, 0) / BN;
+        // V's rows of a diagonal tile, one to a thread: values that are not finite
+        // become zero, their keys are noted
+        auto screen_rows = [&](int j) {
+            const uint32_t inf = 0x7C007C00u;
+            // (a product with zero is 0, or NaN where the value is not finite)
+            const __half2 zero = __halves2half2(__ushort_as_half(0), __ushort_as_half(0));
+            __half2 sum = zero, sum1 = zero;
+            bool w = true;
+#pragma unroll
+            for (int h = 0; h < C::SPT; ++h) {
+                const int at = v_tile(j) * C::SPT + h, slot = at % C::NSLOT;
+                w = w && wait.warp(&full[slot], (uint32_t)(at / C::NSLOT) & 1u);
+                if (!w) return false;
+                const uint8_t *row = smem + C::OFF_RING + slot * C::SLOT + r * 128;
+#pragma unroll
+                for (int c = 0; c < C::SD / 8; ++c) {
+                    // (the order differs by lane: no two of 8 lanes meet in a bank)
+                    const uint4 x = *reinterpret_cast<const uint4 *>(row + (c >> 3) * (BN * 128) + ((c + r) & 7) * 16);
+                    const __half2 *h = reinterpret_cast<const __half2 *>(&x);
+                    sum = __hfma2(h[0], zero, sum);
+                    sum1 = __hfma2(h[1], zero, sum1);
+                    sum = __hfma2(h[2], zero, sum);
+                    sum1 = __hfma2(h[3], zero, sum1);
+                }
+            }
+            sum = __hadd2(sum, sum1);
+            const float both = __low2float(sum) + __high2float(sum);
+            const bool bad = both != both && j * BN + r < job.nk;
+            const uint32_t noted = __ballot_sync(0xffffffffu, bad);
+            if (noted == 0u) return true;
+            if (lane == 0) {
+                atomicOr(&sm_bad[(j - diag0) & 3][w4], noted);
+                sm_any = 1u;
+            }
+            if (bad) {
+#pragma unroll
+                for (int h = 0; h < C::SPT; ++h) {
+                    const int slot = (v_tile(j) * C::SPT + h) % C::NSLOT;
+                    for (int c = 0; c < C::SD / 2; ++c) {
+                        uint32_t *x = reinterpret_cast<uint32_t *>(smem + C::OFF_RING + slot * C::SLOT + (c >> 5) * (BN * 128) + r * 128) + (c & 31);
+                        *x &= ~__vcmpeq2(*x & inf, inf);
+                    }
+                }
+            }
+            fence_proxy_async_smem();
+            return true;
+        };
         auto zero_rows = [&](int j, int keys) {
-            // the last V is the tile 2 j + 1 of the ring in either order of loading
             const int row0 = keys, rows = ((keys + 15) & ~15) - keys;
             bool w = true;
 #pragma unroll
             for (int h = 0; h < C::SPT; ++h) {
-                const int at = (2 * j + 1) * C::SPT + h, slot = at % C::NSLOT;
+                const int at = v_tile(j) * C::SPT + h, slot = at % C::NSLOT;
                 w = w && wait.warp(&full[slot], (uint32_t)(at / C::NSLOT) & 1u);
                 if (!w) return false;
                 for (int x = r; x < rows * (C::SD / 8); x += 128) {
@@ -457,6 +517,11 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         for (int j = 0; j < steps; ++j) {
             const int buf = C::NQ == 1 ? j % C::NS : grp;
             const uint32_t ph = (uint32_t)(C::NQ == 1 ? j / C::NS : j) & 1u;
+            // (here, where no scores are held in registers)
+            if (a.causal && (j + 1) * BN > all_see) {
+                ok = screen_rows(j);
+                if (!ok) break;
+            }
             const uint32_t pcol = lane_base + (uint32_t)(C::P_BESIDE ? C::COL_P + grp * (BN / 2) : buf * BN);
             ok = wait.warp(&sbar[buf], ph);
             if (!ok) break;
@@ -577,6 +642,21 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                 }
             }
         }
+        if (*(volatile uint32_t *)&sm_any && mine) {
+            // noted keys that this row sees (none, as a rule)
+            const volatile uint32_t *noted = &sm_bad[0][0];
+            for (int i = 0; i < 16; ++i)
+                for (uint32_t bits = noted[i]; bits; bits &= bits - 1) {
+                    const int key = (diag0 + (i >> 2)) * BN + (i & 3) * 32 + __ffs(bits) - 1;
+                    if (key >= limit) continue;
+                    const uint16_t *vr = a.v + (size_t)(job.k0 + key) * (size_t)a.ld_v + (size_t)head * D;
+                    for (int d = 0; d < D; ++d) {
+                        const float x = __half2float(__ushort_as_half(vr[d]));
+                        if (!(fabsf(x) <= 65504.0f))
+                            dst[d] = __half_as_ushort(__float2half_rn(__half2float(__ushort_as_half(dst[d])) + x));
+                    }
+                }
+        }
         tc_fence_before();
     }
     __syncthreads();
@@ -627,6 +707,8 @@ w4a8_status launch_prompt_attention(const uint16_t *q, const uint16_t *k, const 
     PromptArgs a = {};
     a.cu_q = cu_q;
     a.cu_k = cu_k;
+    a.v = v;
+    a.ld_v = s.ld_v;
     a.out = out;
     a.Tq = s.Tq;
     a.Tk = s.Tk;

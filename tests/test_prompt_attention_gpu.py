@@ -157,6 +157,37 @@ def test_neighbours_do_not_reach(w4, D, bad):
     assert w4.get_device_status() == 0
 
 
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 3, 1), (128, 1, 1), (128, 8, 1), (256, 4, 2)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_keys_that_a_row_does_not_see_hold_anything(w4, D, Hq, Hkv, bad):
+    # rows before the spoilt keys are as without them, and so are the dimensions
+    # of V that are not spoilt; a row that sees a spoilt value gets it
+    L, at = 400, [70, 131, 250, 399]
+    q, k, v = _inputs(L, L, Hq, Hkv, D, seed=15)
+    qd, kd, vd, cu = q.cuda(), k.cuda(), v.cuda(), _cu([L])
+    clean = w4.prompt_attention(qd, kd, vd, cu)
+    for t in at:
+        kk, vv = kd.clone(), vd.clone()
+        kk[t] = bad
+        vv[t] = bad
+        out = w4.prompt_attention(qd, kk, vv, cu)
+        assert torch.equal(out[:t], clean[:t])
+        assert not bool(torch.isfinite(out[t:]).any())
+        vv = vd.clone()
+        vv[t, :, 5] = bad
+        out = w4.prompt_attention(qd, kd, vv, cu)
+        assert torch.equal(out[:t], clean[:t])
+        rest = torch.ones(D, dtype=torch.bool)
+        rest[5] = False
+        assert torch.equal(out[t:, :, rest.cuda()], clean[t:, :, rest.cuda()])
+        assert not bool(torch.isfinite(out[t:, :, 5]).any())
+        if bad != bad:
+            assert bool(torch.isnan(out[t:, :, 5]).all())
+        else:
+            assert bool((out[t:, :, 5] == bad).all())
+    assert w4.get_device_status() == 0
+
+
 def test_rows_of_no_sequence_stay(w4):
     q, k, v = _inputs(100, 100, 2, 1, 64, seed=3)
     out = torch.full((100, 2, 64), 7.0, dtype=torch.float16, device="cuda")
