@@ -7,7 +7,7 @@ implementation: if the library is missing or the GPU is not sm_103, calls
 raise.
 """
 import ctypes
-import math
+import importlib.util
 import os
 from typing import NamedTuple
 
@@ -37,12 +37,6 @@ class W4A8Error(RuntimeError):
         name = STATUS.get(status, str(status))
         msg = lib().w4a8_status_string(status).decode() if _lib is not None else name
         super().__init__(f"{what}: {name} ({msg})")
-
-
-class _CKv8(ctypes.Structure):
-    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
-                ("v_scale", ctypes.c_void_p), ("pages", ctypes.c_int), ("heads", ctypes.c_int),
-                ("page_tokens", ctypes.c_int), ("dim", ctypes.c_int)]
 
 
 def lib():
@@ -75,18 +69,10 @@ def lib():
         L.w4a8_decode_attention_workspace_bytes.argtypes = [i, i, i, i, i]
         L.w4a8_decode_attention_workspace_bytes.restype = sz
         L.w4a8_decode_attention.argtypes = [P, P, P, P, i, i, i, i, i, P, P, sz, P]
-        ll, f32, C = ctypes.c_longlong, ctypes.c_float, ctypes.POINTER(_CKv8)
-        L.w4a8_prompt_attention.argtypes = [P, P, P, ll, ll, ll, P, P, i, i, i, i, i, i, i, f32, P, P]
-        L.w4a8_kv8_append.argtypes = [C, P, P, ll, ll, P, P, P, i, i, i, P]
-        L.w4a8_kv8_read.argtypes = [C, P, P, i, i, i, P, P, P]
         L.w4a8_decode_attention_kv8_workspace_bytes.argtypes = [i, i, i, i, i, i]
         L.w4a8_decode_attention_kv8_workspace_bytes.restype = sz
-        L.w4a8_decode_attention_kv8.argtypes = [P, C, P, P, i, i, i, f32, P, P, sz, P]
-        L.w4a8_kv8_free_pages.argtypes = [P, P, i, i, i, i, P, P, P]
-        L.w4a8_kv8_fork.argtypes = [C, P, P, P, P, P, i, i, i, P]
         L.w4a8_kv8_compact_workspace_bytes.argtypes = [i]
         L.w4a8_kv8_compact_workspace_bytes.restype = sz
-        L.w4a8_kv8_compact.argtypes = [C, P, P, i, i, P, P, P, sz, P]
         L.w4a8_workspace_bytes.argtypes = [i, i, i, i]
         L.w4a8_workspace_bytes.restype = sz
         L.w4a8_linear.argtypes = [P, P, P, i, i, i, P, P]
@@ -103,11 +89,33 @@ def lib():
         for f in ("w4a8_pack", "w4a8_linear", "w4a8_linear_ex", "w4a8_linear_gated", "w4a8_rmsnorm_quant",
                   "w4a8_linear_q8", "w4a8_decode_attention", "w4a8_linear_prefill_noalloc", "w4a8_debug_quantize_act",
                   "w4a8_debug_block_dots", "w4a8_debug_stream_read", "w4a8_get_device_status", "w4a8_set_wait_budget",
-                  "w4a8_debug_wait_timeout", "w4a8_prompt_attention", "w4a8_kv8_append", "w4a8_kv8_read",
-                  "w4a8_decode_attention_kv8", "w4a8_kv8_free_pages", "w4a8_kv8_fork", "w4a8_kv8_compact"):
+                  "w4a8_debug_wait_timeout"):
             getattr(L, f).restype = i
         _lib = L
     return _lib
+
+
+_native = None
+
+
+def _ext():
+    """The module of csrc/binding.cpp: the newer operators' checks and calls (loaded on first use)."""
+    global _native
+    if _native is None:
+        lib()
+        spec = importlib.util.spec_from_file_location("_w4a8", os.path.join(_HERE, "_build", "_w4a8.so"))
+        if spec is None or not os.path.exists(spec.origin):
+            raise RuntimeError("_build/_w4a8.so is missing (run int4_weight_quantized_gb300.build.build())")
+        _native = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(_native)
+    return _native
+
+
+def _result(r, what):
+    """An entry point's outputs, or W4A8Error where it returned a status."""
+    if r.__class__ is int:
+        raise W4A8Error(r, what)
+    return r
 
 
 def _check(status, what):
@@ -115,24 +123,15 @@ def _check(status, what):
         raise W4A8Error(status, what)
 
 
-# The current stream's handle: torch.cuda.current_stream() builds a Stream
-# object (2.9 us on the GPU's host) around the handle that this returns (0.1 us).
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
 def _stream():
-    if _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
-    return torch.cuda.current_stream().cuda_stream
+    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
 def _p(t):
-    return t.data_ptr() if t is not None else None
+    return ctypes.c_void_p(t.data_ptr()) if t is not None else ctypes.c_void_p(0)
 
 
 def _need(t, dtype, shape, name):
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
-        return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
@@ -328,170 +327,50 @@ def kv8_cache(pages, heads, page_tokens, dim, device="cuda"):
                     torch.zeros(codes, dtype=torch.int8, device=device), torch.zeros(scale, device=device))
 
 
-def _kv8(cache):
-    kc = cache.k_codes
-    if not isinstance(kc, torch.Tensor) or kc.dim() != 4:
-        raise TypeError("k_codes must be a 4-dimensional CUDA tensor")
-    P, H, T, D = kc.shape
-    _need(kc, torch.int8, (P, H, T, D), "k_codes")
-    _need(cache.v_codes, torch.int8, (P, H, T, D), "v_codes")
-    _need(cache.k_scale, torch.float32, (P, H, T // KV8_BLOCK), "k_scale")
-    _need(cache.v_scale, torch.float32, (P, H, T // KV8_BLOCK), "v_scale")
-    return _CKv8(kc.data_ptr(), cache.k_scale.data_ptr(), cache.v_codes.data_ptr(), cache.v_scale.data_ptr(), P, H, T, D)
-
-
-def _need_rows(t, heads, dim, name):
-    """[tokens][heads][dim] fp16, dense but for the stride between tokens (a part of a fused
-    projection's output will do); returns (tokens, elements between tokens)."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype is not torch.float16:
-        raise TypeError(f"{name} must be {torch.float16}, got {t.dtype}")
-    shape = t.shape
-    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
-        raise ValueError(f"{name} must have shape (tokens, {heads}, {dim}), got {tuple(shape)}")
-    ld, inner, one = t.stride()
-    if one != 1 or (heads > 1 and inner != dim):
-        raise ValueError(f"{name}'s heads must be contiguous")
-    return shape[0], ld if shape[0] > 1 else heads * dim
-
-
 def prompt_attention(q, k, v, cu_q, cu_k=None, causal=True, scale=None, out=None):
     """Attention of packed prompts: q fp16 [Tq][Hq][D], k and v fp16 [Tk][Hkv][D] (any stride
-    between tokens), cu_q and cu_k int32 [B+1] (device; cu_k = cu_q when not given), scale
-    1/sqrt(D) when not given -> fp16 [Tq][Hq][D] (w4a8_prompt_attention)."""
-    if q.dim() != 3 or k.dim() != 3:
-        raise ValueError("q, k and v must have shape (tokens, heads, dim)")
-    _, Hq, D = q.shape
-    Hkv = k.shape[1]
-    Tq, ld_q = _need_rows(q, Hq, D, "q")
-    Tk, ld_k = _need_rows(k, Hkv, D, "k")
-    Tv, ld_v = _need_rows(v, Hkv, D, "v")
-    if Tv != Tk:
-        raise ValueError(f"k and v must have as many tokens, got {Tk} and {Tv}")
-    if cu_k is None:
-        cu_k = cu_q
-    B = cu_q.shape[0] - 1
-    _need(cu_q, torch.int32, (B + 1,), "cu_q")
-    _need(cu_k, torch.int32, (B + 1,), "cu_k")
-    if out is None:
-        out = torch.empty((Tq, Hq, D), dtype=torch.float16, device=q.device)
-    _need(out, torch.float16, (Tq, Hq, D), "out")
-    _check(lib().w4a8_prompt_attention(_p(q), _p(k), _p(v), ld_q, ld_k, ld_v, _p(cu_q), _p(cu_k), B, Tq, Tk, Hq, Hkv, D,
-                                       1 if causal else 0, 1.0 / math.sqrt(D) if scale is None else float(scale), _p(out),
-                                       _stream()), "w4a8_prompt_attention")
-    return out
+    between tokens: parts of a fused projection's output will do), cu_q and cu_k int32 [B+1]
+    (device; cu_k = cu_q when not given), scale 1/sqrt(D) when not given -> fp16 [Tq][Hq][D]
+    (w4a8_prompt_attention)."""
+    return _result(_ext().prompt_attention(q, k, v, cu_q, cu_k, causal, scale, out), "w4a8_prompt_attention")
 
 
 def kv8_append(cache, k, v, table, start, cu):
     """Quantise new tokens into the cache: sequence b holds start[b] tokens and gets rows
     cu[b]..cu[b+1]-1 of k and v (fp16 [N][heads][dim], any stride between tokens); table int32
     [B][max_pages], start int32 [B], cu int32 [B+1] (device) (w4a8_kv8_append)."""
-    c = _kv8(cache)
-    n, ld_k = _need_rows(k, c.heads, c.dim, "k")
-    nv, ld_v = _need_rows(v, c.heads, c.dim, "v")
-    if nv != n:
-        raise ValueError(f"k and v must have as many tokens, got {n} and {nv}")
-    B, maxp = table.shape
-    _need(table, torch.int32, (B, maxp), "table")
-    _need(start, torch.int32, (B,), "start")
-    _need(cu, torch.int32, (B + 1,), "cu")
-    _check(lib().w4a8_kv8_append(ctypes.byref(c), _p(k), _p(v), ld_k, ld_v, _p(table), _p(start), _p(cu), B, maxp, n,
-                                 _stream()), "w4a8_kv8_append")
+    _result(_ext().kv8_append(cache, k, v, table, start, cu), "w4a8_kv8_append")
 
 
 def kv8_read(cache, table, cu, total, k_out=None, v_out=None):
     """Read tokens back: sequence b's first cu[b+1]-cu[b] tokens into rows from cu[b] of two
     fp16 [total][heads][dim] tensors, which are returned (w4a8_kv8_read)."""
-    c = _kv8(cache)
-    B, maxp = table.shape
-    _need(table, torch.int32, (B, maxp), "table")
-    _need(cu, torch.int32, (B + 1,), "cu")
-    shape = (int(total), c.heads, c.dim)
-    if k_out is None:
-        k_out = torch.empty(shape, dtype=torch.float16, device=table.device)
-    if v_out is None:
-        v_out = torch.empty(shape, dtype=torch.float16, device=table.device)
-    _need(k_out, torch.float16, shape, "k_out")
-    _need(v_out, torch.float16, shape, "v_out")
-    _check(lib().w4a8_kv8_read(ctypes.byref(c), _p(table), _p(cu), B, maxp, shape[0], _p(k_out), _p(v_out), _stream()),
-           "w4a8_kv8_read")
-    return k_out, v_out
+    return _result(_ext().kv8_read(cache, table, cu, total, k_out, v_out), "w4a8_kv8_read")
 
 
 def decode_attention_kv8(q, cache, table, lens, scale=None, out=None, workspace=None):
     """Decode attention over the 8-bit cache: q fp16 [B][Hq][dim], table int32 [B][max_pages],
     lens int32 [B] (device), scale 1/sqrt(dim) when not given -> fp16 [B][Hq][dim]
     (w4a8_decode_attention_kv8)."""
-    c = _kv8(cache)
-    B, Hq, D = q.shape
-    maxp = table.shape[1]
-    _need(q, torch.float16, (B, Hq, c.dim), "q")
-    _need(table, torch.int32, (B, maxp), "table")
-    _need(lens, torch.int32, (B,), "lens")
-    if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.float16, device=q.device)
-    _need(out, torch.float16, (B, Hq, D), "out")
-    if workspace is None:
-        need = lib().w4a8_decode_attention_kv8_workspace_bytes(B, Hq, c.heads, D, c.page_tokens, maxp)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    _check(lib().w4a8_decode_attention_kv8(_p(q), ctypes.byref(c), _p(table), _p(lens), B, Hq, maxp,
-                                           1.0 / math.sqrt(D) if scale is None else float(scale), _p(out), _p(workspace),
-                                           workspace.numel(), _stream()), "w4a8_decode_attention_kv8")
-    return out
+    return _result(_ext().decode_attention_kv8(q, cache, table, lens, scale, out, workspace), "w4a8_decode_attention_kv8")
 
 
 def kv8_free_pages(cache, table, lens, ids=None, count=None):
     """The pages that no row of table int32 [S][max_pages] holds within lens int32 [S]: (ids
     int32 [pages], ascending, -1 behind the last, count int32 [1]) (w4a8_kv8_free_pages)."""
-    c = _kv8(cache)
-    S, maxp = table.shape
-    _need(table, torch.int32, (S, maxp), "table")
-    _need(lens, torch.int32, (S,), "lens")
-    if ids is None:
-        ids = torch.empty(c.pages, dtype=torch.int32, device=table.device)
-    if count is None:
-        count = torch.empty(1, dtype=torch.int32, device=table.device)
-    _need(ids, torch.int32, (c.pages,), "ids")
-    _need(count, torch.int32, (1,), "count")
-    _check(lib().w4a8_kv8_free_pages(_p(table), _p(lens), S, maxp, c.page_tokens, c.pages, _p(ids), _p(count), _stream()),
-           "w4a8_kv8_free_pages")
-    return ids, count
+    return _result(_ext().kv8_free_pages(cache, table, lens, ids, count), "w4a8_kv8_free_pages")
 
 
 def kv8_fork(cache, table, lens, src, dst, fresh):
     """Rows dst[i] of table and lens become copies of rows src[i] that share its full pages; a
     last page that is not full is copied into page fresh[i] (w4a8_kv8_fork)."""
-    c = _kv8(cache)
-    S, maxp = table.shape
-    n = src.shape[0]
-    _need(table, torch.int32, (S, maxp), "table")
-    _need(lens, torch.int32, (S,), "lens")
-    for t, nm in ((src, "src"), (dst, "dst"), (fresh, "fresh")):
-        _need(t, torch.int32, (n,), nm)
-    _check(lib().w4a8_kv8_fork(ctypes.byref(c), _p(table), _p(lens), _p(src), _p(dst), _p(fresh), n, S, maxp, _stream()),
-           "w4a8_kv8_fork")
+    _result(_ext().kv8_fork(cache, table, lens, src, dst, fresh), "w4a8_kv8_fork")
 
 
 def kv8_compact(cache, table, lens, table_out=None, count=None, workspace=None):
     """Move the held pages to the cache's front: returns (the table with their new numbers, the
     number of held pages int32 [1]); table itself stays as it was (w4a8_kv8_compact)."""
-    c = _kv8(cache)
-    S, maxp = table.shape
-    _need(table, torch.int32, (S, maxp), "table")
-    _need(lens, torch.int32, (S,), "lens")
-    if table_out is None:
-        table_out = torch.empty_like(table)
-    if count is None:
-        count = torch.empty(1, dtype=torch.int32, device=table.device)
-    _need(table_out, torch.int32, (S, maxp), "table_out")
-    _need(count, torch.int32, (1,), "count")
-    if workspace is None:
-        need = lib().w4a8_kv8_compact_workspace_bytes(c.pages)
-        workspace = torch.empty(need, dtype=torch.uint8, device=table.device)
-    _check(lib().w4a8_kv8_compact(ctypes.byref(c), _p(table), _p(lens), S, maxp, _p(table_out), _p(count), _p(workspace),
-                                  workspace.numel(), _stream()), "w4a8_kv8_compact")
-    return table_out, count
+    return _result(_ext().kv8_compact(cache, table, lens, table_out, count, workspace), "w4a8_kv8_compact")
 
 
 def linear_c(x, packed, scales, out):

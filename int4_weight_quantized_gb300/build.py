@@ -2,12 +2,16 @@
 
 Each .cu under csrc/ is compiled by its own nvcc process (in parallel) and
 the objects are linked into one shared library with the CUDA runtime linked
-statically, so loading it needs no CUDA shared libraries.  Rebuilds only
-when a source or header is newer than the library.
+statically, so loading it needs no CUDA shared libraries.  Beside it comes
+_w4a8.so, the Python entry points of binding.cpp, which links the library and
+the torch of this interpreter.  Rebuilds only when a source or header is newer
+than the libraries.
 """
 import glob
 import os
 import subprocess
+import sys
+import sysconfig
 import tempfile
 from concurrent.futures import ThreadPoolExecutor
 
@@ -16,6 +20,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libw4a8.so")
+EXT = os.path.join(OUT_DIR, "_w4a8.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -28,7 +33,7 @@ def _sources():
 
 
 def _deps():
-    return (_sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
+    return (_sources() + glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
             + glob.glob(os.path.join(ROOT, "include", "*.h")) + [__file__])
 
 
@@ -41,28 +46,57 @@ def _compile(src, extra):
     return obj, r.stderr
 
 
+def _compile_binding():
+    import torch
+    top = os.path.join(os.path.dirname(torch.__file__), "include")
+    obj = os.path.join(OUT_DIR, "binding.cpp.o")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", os.path.join(ROOT, "include"), "-isystem", top, "-isystem", os.path.join(top, "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"),
+           "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_binding(obj):
+    import torch
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    fd, tmp = tempfile.mkstemp(suffix=".so", dir=OUT_DIR)
+    os.close(fd)
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", OUT_DIR, "-lw4a8", "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+           "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{libs}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, EXT)
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile csrc/*.cu for sm_103a and link _build/libw4a8.so; returns its path."""
+    """Compile csrc/*.cu for sm_103a and link _build/libw4a8.so (and _w4a8.so); returns the library's path."""
     os.makedirs(OUT_DIR, exist_ok=True)
-    if not force and os.path.exists(LIB):
-        if os.path.getmtime(LIB) >= max(os.path.getmtime(p) for p in _deps()):
+    if not force and os.path.exists(LIB) and os.path.exists(EXT):
+        if min(os.path.getmtime(LIB), os.path.getmtime(EXT)) >= max(os.path.getmtime(p) for p in _deps()):
             return LIB
     extra = list(extra_flags) + (["-Xptxas", "-v"] if verbose else [])
     with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
+        binding = ex.submit(_compile_binding)
         results = list(ex.map(lambda s: _compile(s, extra), _sources()))
+        binding = binding.result()
     if verbose:
         for _, log in results:
             print(log)
     fd, tmp = tempfile.mkstemp(suffix=".so", dir=OUT_DIR)
     os.close(fd)
-    cmd = [NVCC, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *[o for o, _ in results]]
+    cmd = [NVCC, *ARCH, "-shared", "-cudart", "static", "-Xlinker", "-soname=libw4a8.so", "-o", tmp, *[o for o, _ in results]]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(binding)
     return LIB
 
 
 if __name__ == "__main__":
-    import sys
     print(build(force=True, verbose="-v" in sys.argv))

@@ -12,13 +12,29 @@ def w4():
     from int4_weight_quantized_gb300.build import build
     build()
     import int4_weight_quantized_gb300 as w4
-    w4.lib()
+    _declare(w4.lib())
     return w4
 
 
 INVALID, MISALIGNED, WORKSPACE, UNSUPPORTED = 1, 2, 7, 6
 P = ctypes.c_void_p
 GOOD, ODD, NULL = 4096, 4097, 0
+
+
+class _CKv8(ctypes.Structure):
+    _fields_ = [(n, P) for n in ("k_codes", "k_scale", "v_codes", "v_scale")] + [
+        (n, ctypes.c_int) for n in ("pages", "heads", "page_tokens", "dim")]
+
+
+def _declare(L):
+    """The C signatures of include/w4a8.h that the tests call with plain numbers for pointers."""
+    i, sz, ll, f, C = ctypes.c_int, ctypes.c_size_t, ctypes.c_longlong, ctypes.c_float, ctypes.POINTER(_CKv8)
+    for name, args in (("prompt_attention", [P, P, P, ll, ll, ll, P, P, i, i, i, i, i, i, i, f, P, P]),
+                       ("kv8_append", [C, P, P, ll, ll, P, P, P, i, i, i, P]), ("kv8_read", [C, P, P, i, i, i, P, P, P]),
+                       ("decode_attention_kv8", [P, C, P, P, i, i, i, f, P, P, sz, P]),
+                       ("kv8_free_pages", [P, P, i, i, i, i, P, P, P]), ("kv8_fork", [C, P, P, P, P, P, i, i, i, P]),
+                       ("kv8_compact", [C, P, P, i, i, P, P, P, sz, P])):
+        getattr(L, "w4a8_" + name).argtypes = args
 
 
 def _prompt(w4, q=GOOD, k=GOOD, v=GOOD, ld_q=2048, ld_k=256, ld_v=256, cu_q=GOOD, cu_k=GOOD, B=1, Tq=8, Tk=8, Hq=8, Hkv=1,
@@ -44,7 +60,7 @@ def test_prompt_attention_refuses_pointers(w4, bad):
 def _cache(w4, **kw):
     f = dict(k_codes=GOOD, k_scale=GOOD, v_codes=GOOD, v_scale=GOOD, pages=10, heads=2, page_tokens=32, dim=128)
     f.update(kw)
-    return w4._CKv8(*(f[n] for n, _ in w4._CKv8._fields_))
+    return _CKv8(*(f[n] for n, _ in _CKv8._fields_))
 
 
 BAD_CACHES = [(dict(pages=0), INVALID), (dict(heads=0), INVALID), (dict(page_tokens=8), INVALID), (dict(page_tokens=48), INVALID),
