@@ -381,8 +381,8 @@ w4a8_status w4a8_decode_attention_kv8(const uint16_t *q, const w4a8_kv8 *cache, 
     if (st != W4A8_OK) return st;
     if (!decode_kv8_shape_ok(B, Hq, c.Hkv, c.D, c.T, max_pages) || !scale_ok(scale)) return W4A8_ERR_INVALID_VALUE;
     if (!aligned16(q) || !aligned16(out) || !aligned4(table) || !aligned4(lens)) return W4A8_ERR_MISALIGNED;
-    if (!aligned16(workspace) || workspace_bytes < kv8_decode_workspace_bytes(B, Hq, c.Hkv, c.D, c.T, max_pages))
-        return W4A8_ERR_WORKSPACE;
+    const size_t need = kv8_decode_workspace_bytes(B, Hq, c.Hkv, c.D, c.T, max_pages);
+    if (need && (!aligned16(workspace) || workspace_bytes < need)) return W4A8_ERR_WORKSPACE;
     st = check_device();
     if (st != W4A8_OK) return st;
     cudaGetLastError();

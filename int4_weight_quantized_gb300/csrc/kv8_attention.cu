@@ -44,6 +44,7 @@
 #include "kernels.h"
 #include "kv8.cuh"
 #include "sync.cuh"
+#include "tc.cuh"
 
 namespace {
 
@@ -53,6 +54,7 @@ constexpr int W = 8;                 // warps per CTA
 constexpr int TILE = 64;             // tokens per unit of the split
 constexpr int MAXC = 152 * 2;        // CTAs at most
 constexpr int MAXW = MAXC * W;       // workers (warps) at most
+constexpr int PAIR_TOKENS = 1024;    // tokens that a table may hold for the pair kernel
 constexpr float kTiny = 8.673617e-19f;   // 2^-60: stands for a zero scale in the weights (the smallest
                                          // real one, from the smallest fp16 value, is 2^-31)
 
@@ -262,6 +264,142 @@ __device__ __forceinline__ void load_v(uint32_t vb, int g, int t, uint32_t (&v)[
     }
 }
 
+// One block of 16 tokens (K at kb, V behind it; `left` of them are the
+// sequence's): S^T, the softmax step, O^T.  ks: the block's K scale times
+// scale log2 e; vs: its V scale.
+template <int D, int NT>
+__device__ __forceinline__ void add_block(uint32_t kb, float ks, float vs, int left, int g, int t, const uint32_t (&qf)[NT][D / 16][2],
+                                          float (&o)[NT][D / 16][4], float (&m)[NT][2], float (&l)[NT][2]) {
+    constexpr int NJ = D / 16;
+    const uint32_t vb = kb + Ring<D>::HALF;
+    float s[NT][4], s2[NT][4];                // two sums: shorter chains of products
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[n][e] = s2[n][e] = 0.0f;
+    {
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) {
+            const int c = k_piece<D>(t, j);
+            const uint4 kl = lds16(kb + (uint32_t)piece<D>(g, c)), kh = lds16(kb + (uint32_t)piece<D>(g + 8, c));
+            const uint32_t lo[4] = {kl.x, kl.y, kl.z, kl.w}, hi[4] = {kh.x, kh.y, kh.z, kh.w};
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const uint32_t p = lo[w] ^ 0x80808080u, r = hi[w] ^ 0x80808080u;
+                const uint32_t a0 = codes_half2<0x4140>(p), a2 = codes_half2<0x4342>(p);
+                const uint32_t a1 = codes_half2<0x4140>(r), a3 = codes_half2<0x4342>(r);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    mma16816(w & 1 ? s2[n] : s[n], a0, a1, a2, a3, qf[n][4 * j + w][0], qf[n][4 * j + w][1]);
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[n][e] += s2[n][e];
+    }
+
+    uint32_t pf[NT][2];
+    {
+        const float wv = vs > 0.0f ? vs : kTiny;
+        const float lw = lg2(wv), iw = rcp(wv);
+        const bool in0 = g < left, in1 = g + 8 < left;
+        float y[NT][4];
+        bool move = false;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            y[n][0] = in0 ? fmaf(s[n][0], ks, lw) : -INFINITY;
+            y[n][1] = in0 ? fmaf(s[n][1], ks, lw) : -INFINITY;
+            y[n][2] = in1 ? fmaf(s[n][2], ks, lw) : -INFINITY;
+            y[n][3] = in1 ? fmaf(s[n][3], ks, lw) : -INFINITY;
+            move = move || fmaxf(y[n][0], y[n][2]) > m[n][0] + 8.0f || fmaxf(y[n][1], y[n][3]) > m[n][1] + 8.0f;
+        }
+        if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float v = fmaxf(y[n][e], y[n][e + 2]);
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+                    const float mn = fmaxf(m[n][e], v);
+                    const float f = m[n][e] == -INFINITY ? 0.0f : ex2(m[n][e] - mn);
+                    m[n][e] = mn;
+                    l[n][e] *= f;
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j) {
+                        o[n][j][e] *= f;
+                        o[n][j][e + 2] *= f;
+                    }
+                }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float p[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                p[e] = ex2(y[n][e] - m[n][e & 1]);
+                l[n][e & 1] = fmaf(p[e], iw, l[n][e & 1]);
+            }
+            const __half2 h0 = __floats2half2_rn(p[0], p[1]), h1 = __floats2half2_rn(p[2], p[3]);
+            pf[n][0] = transpose8(*reinterpret_cast<const uint32_t *>(&h0));
+            pf[n][1] = transpose8(*reinterpret_cast<const uint32_t *>(&h1));
+        }
+        uint32_t v[4][D / 32];
+        load_v<D>(vb, g, t, v);
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w) {
+            const uint32_t v0 = v[0][w] ^ 0x80808080u, v1 = v[1][w] ^ 0x80808080u;
+            const uint32_t v2 = v[2][w] ^ 0x80808080u, v3 = v[3][w] ^ 0x80808080u;
+            // bytes 0 1 and 2 3 of the four tokens, two tokens side by side
+            const uint32_t p0 = __byte_perm(v0, v1, 0x5140), p1 = __byte_perm(v0, v1, 0x7362);
+            const uint32_t r0 = __byte_perm(v2, v3, 0x5140), r1 = __byte_perm(v2, v3, 0x7362);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const uint32_t pp = e ? p1 : p0, rr = e ? r1 : r0;
+                const uint32_t a0 = codes_half2<0x4140>(pp), a1 = codes_half2<0x4342>(pp);
+                const uint32_t a2 = codes_half2<0x4140>(rr), a3 = codes_half2<0x4342>(rr);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma16816(o[n][2 * w + e], a0, a1, a2, a3, pf[n][0], pf[n][1]);
+            }
+        }
+    }
+}
+
+// q of a KV head's group as the products' B operand: head g of each tile of 8
+// (zero past the group).
+template <int D, int NT>
+__device__ __forceinline__ void load_q(const DecodeArgs &a, size_t row0, int g, int t, uint32_t (&qf)[NT][D / 16][2]) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const uint16_t *qp = a.q + (row0 + 8 * n + g) * D;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                if (8 * n + g < a.G) w = *reinterpret_cast<const uint4 *>(qp + 16 * k_piece<D>(t, i) + 8 * e);
+                qf[n][4 * i + 2 * e][0] = w.x;
+                qf[n][4 * i + 2 * e][1] = w.y;
+                qf[n][4 * i + 2 * e + 1][0] = w.z;
+                qf[n][4 * i + 2 * e + 1][1] = w.w;
+            }
+    }
+}
+
+template <int D, int NT>
+__device__ __forceinline__ void clear(float (&o)[NT][D / 16][4], float (&m)[NT][2], float (&l)[NT][2]) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[n][j][e] = 0.0f;
+        m[n][0] = m[n][1] = -INFINITY;
+        l[n][0] = l[n][1] = 0.0f;
+    }
+}
+
 // NT: tiles of 8 query heads (1: up to 8 heads per KV head, 2: up to 16).
 template <int D, int NT>
 __global__ void __launch_bounds__(W * 32, D == 256 || NT == 2 ? 1 : 2) kv8_decode_kernel(const DecodeArgs a) {
@@ -339,34 +477,11 @@ __global__ void __launch_bounds__(W * 32, D == 256 || NT == 2 ? 1 : 2) kv8_decod
     int stage = 0;
 
     while (true) {
-        // a segment: q as the products' B operand, head g of each tile of 8 (zero past the group)
-        uint32_t qf[NT][D / 16][2];
         const size_t row0 = ((size_t)get.b * a.Hkv + get.head) * (size_t)a.G;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const uint16_t *qp = a.q + (row0 + 8 * n + g) * D;
-#pragma unroll
-            for (int i = 0; i < D / 64; ++i)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    uint4 w = make_uint4(0u, 0u, 0u, 0u);
-                    if (8 * n + g < a.G) w = *reinterpret_cast<const uint4 *>(qp + 16 * k_piece<D>(t, i) + 8 * e);
-                    qf[n][4 * i + 2 * e][0] = w.x;
-                    qf[n][4 * i + 2 * e][1] = w.y;
-                    qf[n][4 * i + 2 * e + 1][0] = w.z;
-                    qf[n][4 * i + 2 * e + 1][1] = w.w;
-                }
-        }
+        uint32_t qf[NT][D / 16][2];
+        load_q<D, NT>(a, row0, g, t, qf);
         float o[NT][NJ][4], m[NT][2], l[NT][2];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-#pragma unroll
-            for (int j = 0; j < NJ; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[n][j][e] = 0.0f;
-            m[n][0] = m[n][1] = -INFINITY;
-            l[n][0] = l[n][1] = 0.0f;
-        }
+        clear<D, NT>(o, m, l);
 
         for (; get.blk < get.end; ++get.blk) {
             const int left = get.len - get.blk * 16;         // tokens from the block's first
@@ -376,101 +491,10 @@ __global__ void __launch_bounds__(W * 32, D == 256 || NT == 2 ? 1 : 2) kv8_decod
             __syncwarp();
             issue(stage == 0 ? R::S - 1 : stage - 1);
             const bool ok = (there >> stage) & 1u;
-            const uint32_t kb = ring + (uint32_t)(stage * R::STAGE), vb = kb + R::HALF;
+            const uint32_t kb = ring + (uint32_t)(stage * R::STAGE);
             const float ks = sm_sc[warp][stage][0] * a.scale_log2, vs = sm_sc[warp][stage][1];
             stage = stage == R::S - 1 ? 0 : stage + 1;
-            float s[NT][4], s2[NT][4];                // two sums: shorter chains of products
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[n][e] = s2[n][e] = 0.0f;
-            if (ok) {
-#pragma unroll
-                for (int j = 0; j < D / 64; ++j) {
-                    const int c = k_piece<D>(t, j);
-                    const uint4 kl = lds16(kb + (uint32_t)piece<D>(g, c)), kh = lds16(kb + (uint32_t)piece<D>(g + 8, c));
-                    const uint32_t lo[4] = {kl.x, kl.y, kl.z, kl.w}, hi[4] = {kh.x, kh.y, kh.z, kh.w};
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        const uint32_t p = lo[w] ^ 0x80808080u, r = hi[w] ^ 0x80808080u;
-                        const uint32_t a0 = codes_half2<0x4140>(p), a2 = codes_half2<0x4342>(p);
-                        const uint32_t a1 = codes_half2<0x4140>(r), a3 = codes_half2<0x4342>(r);
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-                            mma16816(w & 1 ? s2[n] : s[n], a0, a1, a2, a3, qf[n][4 * j + w][0], qf[n][4 * j + w][1]);
-                    }
-                }
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) s[n][e] += s2[n][e];
-            }
-
-            uint32_t pf[NT][2];
-            if (ok) {
-                const float wv = vs > 0.0f ? vs : kTiny;
-                const float lw = lg2(wv), iw = rcp(wv);
-                const bool in0 = g < left, in1 = g + 8 < left;
-                float y[NT][4];
-                bool move = false;
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    y[n][0] = in0 ? fmaf(s[n][0], ks, lw) : -INFINITY;
-                    y[n][1] = in0 ? fmaf(s[n][1], ks, lw) : -INFINITY;
-                    y[n][2] = in1 ? fmaf(s[n][2], ks, lw) : -INFINITY;
-                    y[n][3] = in1 ? fmaf(s[n][3], ks, lw) : -INFINITY;
-                    move = move || fmaxf(y[n][0], y[n][2]) > m[n][0] + 8.0f || fmaxf(y[n][1], y[n][3]) > m[n][1] + 8.0f;
-                }
-                if (__any_sync(0xffffffffu, move)) {
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float v = fmaxf(y[n][e], y[n][e + 2]);
-#pragma unroll
-                            for (int d = 4; d < 32; d <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
-                            const float mn = fmaxf(m[n][e], v);
-                            const float f = m[n][e] == -INFINITY ? 0.0f : ex2(m[n][e] - mn);
-                            m[n][e] = mn;
-                            l[n][e] *= f;
-#pragma unroll
-                            for (int j = 0; j < NJ; ++j) {
-                                o[n][j][e] *= f;
-                                o[n][j][e + 2] *= f;
-                            }
-                        }
-                }
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    float p[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        p[e] = ex2(y[n][e] - m[n][e & 1]);
-                        l[n][e & 1] = fmaf(p[e], iw, l[n][e & 1]);
-                    }
-                    const __half2 h0 = __floats2half2_rn(p[0], p[1]), h1 = __floats2half2_rn(p[2], p[3]);
-                    pf[n][0] = transpose8(*reinterpret_cast<const uint32_t *>(&h0));
-                    pf[n][1] = transpose8(*reinterpret_cast<const uint32_t *>(&h1));
-                }
-                uint32_t v[4][D / 32];
-                load_v<D>(vb, g, t, v);
-#pragma unroll
-                for (int w = 0; w < D / 32; ++w) {
-                    const uint32_t v0 = v[0][w] ^ 0x80808080u, v1 = v[1][w] ^ 0x80808080u;
-                    const uint32_t v2 = v[2][w] ^ 0x80808080u, v3 = v[3][w] ^ 0x80808080u;
-                    // bytes 0 1 and 2 3 of the four tokens, two tokens side by side
-                    const uint32_t p0 = __byte_perm(v0, v1, 0x5140), p1 = __byte_perm(v0, v1, 0x7362);
-                    const uint32_t r0 = __byte_perm(v2, v3, 0x5140), r1 = __byte_perm(v2, v3, 0x7362);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const uint32_t pp = e ? p1 : p0, rr = e ? r1 : r0;
-                        const uint32_t a0 = codes_half2<0x4140>(pp), a1 = codes_half2<0x4342>(pp);
-                        const uint32_t a2 = codes_half2<0x4140>(rr), a3 = codes_half2<0x4342>(rr);
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) mma16816(o[n][2 * w + e], a0, a1, a2, a3, pf[n][0], pf[n][1]);
-                    }
-                }
-            }
+            if (ok) add_block<D, NT>(kb, ks, vs, left, g, t, qf, o, m, l);
         }
 
         // the segment's end: l over the lanes, then out, or this part to the workspace
@@ -518,6 +542,168 @@ __global__ void __launch_bounds__(W * 32, D == 256 || NT == 2 ? 1 : 2) kv8_decod
     }
     if (bad && lane == 0) atomicExch(a.status, (int)W4A8_ERR_PAGE);
     asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// A short cache: one cluster per (sequence, KV head), its CTAs' warps taking the
+// sequence's blocks in turn, merged in shared memory and then through distributed
+// shared memory (the same sums as above).  One launch and no workspace; used
+// where the tables hold no more than PAIR_TOKENS tokens and all clusters fit the
+// GPU at once (launch_kv8_decode has the rule).
+template <int D, int NT>
+__global__ void __launch_bounds__(W * 32, 1) kv8_decode_pair_kernel(const DecodeArgs a) {
+    using R = Ring<D>;
+    constexpr int NJ = D / 16, NH = 8 * NT, LD = D + 4;      // a head's row in shared memory, padded against bank conflicts
+    extern __shared__ __align__(128) uint8_t smem[];         // the rings; at the end O [W][NH][LD], then the CTA's [NH][D]
+    float *sm_o = reinterpret_cast<float *>(smem);
+    __shared__ float sm_sc[W][R::S][2];
+    __shared__ float sm_m[W][NH], sm_l[W][NH], sm_ml[2][NH], sm_w[8][NH];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int rank = blockIdx.x, CL = gridDim.x, head = blockIdx.y, b = blockIdx.z;
+    const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * R::S * R::STAGE), ring_sc = smem_u32(&sm_sc[warp][0][0]);
+    const size_t row0 = ((size_t)b * a.Hkv + head) * (size_t)a.G;
+    const int step = CL * W, cap = a.maxp << (a.T_log2 - 4);         // blocks that the table can hold
+    auto page_of = [&](int i) { return i < cap ? kv8::page_at(a.table, b, a.maxp, (i * 16) >> a.T_log2, a.P) : -1; };
+    // the first blocks' pages, the length and q are on the way together
+    int page[R::S];
+#pragma unroll
+    for (int s = 0; s < R::S; ++s) page[s] = page_of(s * step + rank * W + warp);
+    const int len = seq_len(a, b), nblk = (len + 15) >> 4;
+    uint32_t qf[NT][D / 16][2];
+    load_q<D, NT>(a, row0, g, t, qf);
+    uint32_t there = 0u;
+    bool bad = false;
+    auto issue = [&](int i, int stage, int pg) {
+        there &= ~(1u << stage);
+        if (i < nblk) {
+            if (pg >= 0) {
+                copy_block<D>(a, ring + (uint32_t)(stage * R::STAGE), ring_sc + 8u * (uint32_t)stage, pg, head, (i * 16) & (a.T - 1), lane);
+                there |= 1u << stage;
+            } else {
+                bad = true;
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    const int first = rank * W + warp;
+#pragma unroll
+    for (int s = 0; s < R::S - 1; ++s) issue(first + s * step, s, page[s]);
+    int ahead = page[R::S - 1];
+    float o[NT][NJ][4], m[NT][2], l[NT][2];
+    clear<D, NT>(o, m, l);
+    int stage = 0;
+    for (int i = first; i < nblk; i += step) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(R::S - 2) : "memory");
+        __syncwarp();
+        issue(i + (R::S - 1) * step, stage == 0 ? R::S - 1 : stage - 1, ahead);
+        ahead = page_of(i + R::S * step);
+        if ((there >> stage) & 1u)
+            add_block<D, NT>(ring + (uint32_t)(stage * R::STAGE), sm_sc[warp][stage][0] * a.scale_log2, sm_sc[warp][stage][1], len - i * 16, g, t,
+                             qf, o, m, l);
+        stage = stage == R::S - 1 ? 0 : stage + 1;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (bad && lane == 0) atomicExch(a.status, (int)W4A8_ERR_PAGE);
+
+    // the CTA's warps: M = max m_w, O = sum 2^(m_w - M) O_w, L likewise (warp order)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], d);
+            if (g == 0) {
+                sm_m[warp][8 * n + 2 * t + e] = m[n][e];
+                sm_l[warp][8 * n + 2 * t + e] = l[n][e];
+            }
+        }
+    __syncthreads();                                  // also: every warp is done with its ring
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int h = 8 * n + 2 * t + e;
+            float M = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < W; ++w) M = fmaxf(M, sm_m[w][h]);
+            const float f = m[n][e] == -INFINITY ? 0.0f : ex2(m[n][e] - M);
+            float *to = sm_o + ((size_t)warp * NH + h) * LD;
+#pragma unroll
+            for (int j = 0; j < NJ; j += 2)
+                *reinterpret_cast<float4 *>(to + row_dim<D>(j, 0, g)) =
+                    make_float4(o[n][j][e] * f, o[n][j][e + 2] * f, o[n][j + 1][e] * f, o[n][j + 1][e + 2] * f);
+        }
+    if (threadIdx.x < NH) {
+        const int h = threadIdx.x;
+        float M = -INFINITY, L = 0.0f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) M = fmaxf(M, sm_m[w][h]);
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+            if (sm_m[w][h] != -INFINITY) L = fmaf(sm_l[w][h], ex2(sm_m[w][h] - M), L);
+        sm_ml[0][h] = M;
+        sm_ml[1][h] = L;
+    }
+    __syncthreads();
+    auto cta_sum = [&](int i) {                       // four values of head i / D
+        const int h = i / D, d = i % D;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            const float4 x = *reinterpret_cast<const float4 *>(sm_o + ((size_t)w * NH + h) * LD + d);
+            v.x += x.x;
+            v.y += x.y;
+            v.z += x.z;
+            v.w += x.w;
+        }
+        return v;
+    };
+    auto put = [&](int i, float4 v, float L) {
+        const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+        const __half2 lo = __floats2half2_rn(v.x * inv, v.y * inv), hi = __floats2half2_rn(v.z * inv, v.w * inv);
+        uint2 pk;
+        pk.x = *reinterpret_cast<const uint32_t *>(&lo);
+        pk.y = *reinterpret_cast<const uint32_t *>(&hi);
+        *reinterpret_cast<uint2 *>(a.out + row0 * D + i) = pk;
+    };
+    if (CL == 1) {
+        for (int i = threadIdx.x * 4; i < a.G * D; i += W * 128) put(i, cta_sum(i), sm_ml[1][i / D]);
+        return;
+    }
+    float *part = sm_o + (size_t)W * NH * LD;
+    for (int i = threadIdx.x * 4; i < a.G * D; i += W * 128) *reinterpret_cast<float4 *>(part + i) = cta_sum(i);
+    cluster_sync_all();
+    // the cluster's CTAs, in rank order; this CTA writes its share of the outputs
+    if (threadIdx.x < NH) {
+        const int h = threadIdx.x;
+        float mr[8], M = -INFINITY, L = 0.0f;
+        for (int r = 0; r < CL; ++r) {
+            mr[r] = ld_dsmem_f32(dsmem_addr(smem_u32(&sm_ml[0][h]), (uint32_t)r));
+            M = fmaxf(M, mr[r]);
+        }
+        for (int r = 0; r < CL; ++r) {
+            const float w = mr[r] == -INFINITY ? 0.0f : ex2(mr[r] - M);
+            sm_w[r][h] = w;
+            L = fmaf(ld_dsmem_f32(dsmem_addr(smem_u32(&sm_ml[1][h]), (uint32_t)r)), w, L);
+        }
+        sm_m[0][h] = L;
+    }
+    __syncthreads();
+    for (int i = (rank * W * 32 + threadIdx.x) * 4; i < a.G * D; i += CL * W * 128) {
+        const int h = i / D;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int r = 0; r < CL; ++r) {
+            const float4 x = ld_dsmem_f32x4(dsmem_addr(smem_u32(part + i), (uint32_t)r));
+            const float w = sm_w[r][h];
+            v.x = fmaf(x.x, w, v.x);
+            v.y = fmaf(x.y, w, v.y);
+            v.z = fmaf(x.z, w, v.z);
+            v.w = fmaf(x.w, w, v.w);
+        }
+        put(i, v, sm_m[0][h]);
+    }
+    cluster_sync_all();                               // no CTA leaves while a peer may still read its part
 }
 
 // One CTA per (query head, sequence) and share of d: nothing where the pair was
@@ -626,6 +812,45 @@ int split_workers(int B, int Hq, int Hkv, int D, int T, int maxp) {
     return most < warps ? (int)most : warps;
 }
 
+// CTAs of a pair's cluster for the pair kernel, 0 where the split kernel runs.
+// The pair kernel saves the second launch and the parts' way through memory; a
+// sequence is bound to its cluster, so it is for caches whose longest sequence
+// one cluster reads in a few microseconds.  PAIRMEASURE
+int pair_ctas(int B, int Hkv, int T, int maxp) {
+    const long long cap = (long long)maxp * T, pairs = (long long)B * Hkv;
+    if (cap > PAIR_TOKENS || pairs > 152) return 0;
+    int k = 8;
+    while (k > 1 && (pairs * k > 152 || k * W * 16 > cap * 2)) k /= 2;
+    return k;
+}
+
+template <int D, int NT>
+w4a8_status launch_pair(const DecodeArgs &a, int k, cudaStream_t stream) {
+    static std::atomic<int> attr_done[w4a8_host::kDeviceSlots];
+    constexpr int merge = (W * 8 * NT * (D + 4) + 8 * NT * D) * 4, smem = Ring<D>::BYTES > merge ? Ring<D>::BYTES : merge;
+    const w4a8_status st = w4a8_host::ensure_smem_limit(kv8_decode_pair_kernel<D, NT>, smem, attr_done);
+    if (st != W4A8_OK) return st;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)k, (unsigned)a.Hkv, (unsigned)a.B);
+    cfg.blockDim = dim3(W * 32);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)k;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, kv8_decode_pair_kernel<D, NT>, a) != cudaSuccess) {
+        cudaGetLastError();
+        return W4A8_ERR_CUDA;
+    }
+    return w4a8_host::launch_status();
+}
+
 template <int D, int NT>
 w4a8_status launch_decode(const DecodeArgs &a, int C, cudaStream_t stream) {
     static std::atomic<int> attr_done[w4a8_host::kDeviceSlots];
@@ -642,6 +867,7 @@ size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 namespace w4a8_host {
 
 size_t kv8_decode_workspace_bytes(int B, int Hq, int Hkv, int D, int T, int maxp) {
+    if (pair_ctas(B, Hkv, T, maxp) > 0) return 0;
     const size_t rows = (size_t)2 * split_workers(B, Hq, Hkv, D, T, maxp) * (Hq / Hkv);
     return align256(rows * D * 4) + align256(rows * 2 * 4) + (size_t)B * Hkv * sizeof(int2);
 }
@@ -674,6 +900,11 @@ w4a8_status launch_kv8_decode(const uint16_t *q, const Kv8Cache &c, const int32_
     a.scale_log2 = scale * 1.4426950408889634f;
     a.status = device_status_ptr();
     if (!a.status) return W4A8_ERR_CUDA;
+    if (const int k = pair_ctas(B, c.Hkv, c.T, maxp)) {
+        if (c.D == 64) return G <= 8 ? launch_pair<64, 1>(a, k, stream) : launch_pair<64, 2>(a, k, stream);
+        if (c.D == 128) return G <= 8 ? launch_pair<128, 1>(a, k, stream) : launch_pair<128, 2>(a, k, stream);
+        return G <= 8 ? launch_pair<256, 1>(a, k, stream) : launch_pair<256, 2>(a, k, stream);
+    }
     w4a8_status st = W4A8_ERR_UNSUPPORTED;
     if (c.D == 64) st = G <= 8 ? launch_decode<64, 1>(a, C, stream) : launch_decode<64, 2>(a, C, stream);
     if (c.D == 128) st = G <= 8 ? launch_decode<128, 1>(a, C, stream) : launch_decode<128, 2>(a, C, stream);

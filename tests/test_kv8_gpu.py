@@ -214,6 +214,28 @@ def test_decode_attention(w4, D, Hq, H, T):
     assert w4.get_device_status() == 0
 
 
+@pytest.mark.parametrize("B", [1, 5, 20, 75, 150])
+@pytest.mark.parametrize("D,Hq,H,T", [(64, 8, 1, 16), (64, 24, 2, 128), (128, 4, 2, 32), (128, 11, 1, 64), (256, 8, 1, 64), (256, 16, 1, 16)])
+def test_decode_short_tables(w4, D, Hq, H, T, B):
+    # tables of up to 1024 tokens: clusters of 8, 4, 2 and 1 CTAs for each pair,
+    # sequences shorter than a cluster's warps and as long as the table
+    if B * H > 152:
+        B = 152 // H
+    rs = np.random.RandomState(B + D)
+    lens = [[1024, 0, 1, 16, 17, 640, 1009, 127, 128, 129][i] if i < 10 else int(rs.randint(0, 400)) for i in range(B)]
+    P = sum(-(-n // T) for n in lens) + 2
+    cache = _random_cache(w4, P, H, T, D, seed=T)
+    table = _table(lens, T, P, seed=2)
+    q = torch.randn((B, Hq, D), generator=torch.Generator().manual_seed(D)).half()
+    out = w4.decode_attention_kv8(q.cuda(), cache, _i32(table), _i32(lens))
+    _verify_decode(out, q, cache, table, lens, T)
+    # the same tables made longer take the other kernels
+    wide = np.concatenate([table, np.full((B, 1024 // T + 1), -1, np.int32)], 1)
+    other = w4.decode_attention_kv8(q.cuda(), cache, _i32(wide), _i32(lens))
+    _verify_decode(other, q, cache, table, lens, T)
+    assert w4.get_device_status() == 0
+
+
 @pytest.mark.parametrize("D,T", [(64, 16), (128, 32), (256, 128)])
 def test_decode_long_and_short(w4, D, T):
     # one long sequence over many CTAs, cut at any place, among short ones
@@ -495,7 +517,7 @@ def test_refusals(w4):
     with pytest.raises(w4.W4A8Error):
         w4.decode_attention_kv8(q[:, :3].contiguous(), cache, table, lens)
     with pytest.raises(w4.W4A8Error):
-        w4.decode_attention_kv8(q, cache, table, lens, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        w4.decode_attention_kv8(q, cache, table.repeat(1, 100), lens, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ValueError):
         w4.kv8_append(cache, q, q, table, lens, _cu([1]))
     with pytest.raises(TypeError):
