@@ -54,7 +54,7 @@ constexpr int W = 8;                 // warps per CTA
 constexpr int TILE = 64;             // tokens per unit of the split
 constexpr int MAXC = 152 * 2;        // CTAs at most
 constexpr int MAXW = MAXC * W;       // workers (warps) at most
-constexpr int PAIR_TOKENS = 1024;    // tokens that a table may hold for the pair kernel
+constexpr int PAIR_TOKENS = 4096;    // tokens that a table may hold for the pair kernel
 constexpr float kTiny = 8.673617e-19f;   // 2^-60: stands for a zero scale in the weights (the smallest
                                          // real one, from the smallest fp16 value, is 2^-31)
 
@@ -547,8 +547,7 @@ __global__ void __launch_bounds__(W * 32, D == 256 || NT == 2 ? 1 : 2) kv8_decod
 // A short cache: one cluster per (sequence, KV head), its CTAs' warps taking the
 // sequence's blocks in turn, merged in shared memory and then through distributed
 // shared memory (the same sums as above).  One launch and no workspace; used
-// where the tables hold no more than PAIR_TOKENS tokens and all clusters fit the
-// GPU at once (launch_kv8_decode has the rule).
+// where the tables hold no more than PAIR_TOKENS tokens.
 template <int D, int NT>
 __global__ void __launch_bounds__(W * 32, 1) kv8_decode_pair_kernel(const DecodeArgs a) {
     using R = Ring<D>;
@@ -813,13 +812,17 @@ int split_workers(int B, int Hq, int Hkv, int D, int T, int maxp) {
 }
 
 // CTAs of a pair's cluster for the pair kernel, 0 where the split kernel runs.
-// The pair kernel saves the second launch and the parts' way through memory; a
-// sequence is bound to its cluster, so it is for caches whose longest sequence
-// one cluster reads in a few microseconds.  PAIRMEASURE
+// The pair kernel saves the second launch and the parts' way through memory,
+// but a sequence is bound to its cluster.  Measured (split / pair, us, pairs of
+// D = 128): tables of 512 tokens 12.3 / 9.6 for one pair, 22.6 / 8.9 for 152,
+// 34.9 / 22.9 for 600; of 4096 tokens 12.5 / 11.7, 42.6 / 31.7, 123.8 / 100.4
+// where all are full and 13.4 / 12.0, 34.1 / 29.7, 76.4 / 70.3 where their
+// lengths are spread; of 8192 tokens 14.4 / 15.0 for one pair and, spread, 45.8
+// / 52.6 for 152.  So the split kernel takes over above 4096.
 int pair_ctas(int B, int Hkv, int T, int maxp) {
     const long long cap = (long long)maxp * T, pairs = (long long)B * Hkv;
-    if (cap > PAIR_TOKENS || pairs > 152) return 0;
-    int k = 8;
+    if (cap > PAIR_TOKENS) return 0;
+    int k = 8;                           // a portable cluster; all clusters at once, at most two warps to a block
     while (k > 1 && (pairs * k > 152 || k * W * 16 > cap * 2)) k /= 2;
     return k;
 }

@@ -96,8 +96,8 @@ def test_cache_calls_refuse_arguments(w4):
         assert decode(**bad) == INVALID, bad
     for bad in (dict(q=GOOD + 8), dict(out=NULL), dict(table=ODD), dict(lens=NULL)):
         assert decode(**bad) == MISALIGNED, bad
-    need = L.w4a8_decode_attention_kv8_workspace_bytes(1, 8, 2, 128, 32, 64)
-    assert decode(maxp=64, n=need - 1) == WORKSPACE and decode(maxp=64, ws=NULL) == WORKSPACE and decode(maxp=64, ws=GOOD + 4) == WORKSPACE
+    need = L.w4a8_decode_attention_kv8_workspace_bytes(1, 8, 2, 128, 32, 200)
+    assert decode(maxp=200, n=need - 1) == WORKSPACE and decode(maxp=200, ws=NULL) == WORKSPACE and decode(maxp=200, ws=GOOD + 4) == WORKSPACE
 
     assert L.w4a8_kv8_read(c, GOOD, GOOD, 1, 4, -1, GOOD, GOOD, None) == INVALID
     assert L.w4a8_kv8_read(c, GOOD, GOOD, 1, 4, 8, GOOD + 8, GOOD, None) == MISALIGNED
@@ -118,8 +118,8 @@ def test_workspace_sizes(w4):
     ws = L.w4a8_decode_attention_kv8_workspace_bytes
     assert ws(1, 8, 1, 96, 32, 4) == 0 and ws(1, 8, 3, 128, 32, 4) == 0 and ws(1, 32, 1, 128, 32, 4) == 0
     assert ws(0, 8, 1, 128, 32, 4) == 0 and ws(1, 8, 1, 128, 20, 4) == 0
-    assert ws(1, 8, 1, 128, 16, 64) == 0 and ws(152, 8, 1, 128, 64, 16) == 0      # one cluster a pair: no parts
-    assert ws(1, 8, 1, 128, 16, 65) > 0 and ws(153, 8, 1, 128, 16, 64) > 0
+    assert ws(1, 8, 1, 128, 16, 256) == 0 and ws(500, 8, 1, 128, 64, 64) == 0      # one cluster a pair: no parts
+    assert ws(1, 8, 1, 128, 16, 257) > 0 and ws(500, 8, 1, 128, 64, 65) > 0
     assert ws(64, 32, 8, 128, 32, 4096) == ws(64, 32, 8, 128, 32, 512)        # independent of the length
     assert L.w4a8_kv8_compact_workspace_bytes(0) == 0 and L.w4a8_kv8_compact_workspace_bytes(12582913) == 0
     assert L.w4a8_kv8_compact_workspace_bytes(100) >= 4 * (100 + 2 * 51 + 1)

@@ -199,14 +199,15 @@ def _verify_decode(out, q, cache, table, lens, T, scale=None):
             check(out[b, rows], ref, bound, f"sequence {b} of {n} tokens, KV head {h}")
 
 
+@pytest.mark.parametrize("extra", [2, 300])         # tables for either kernel
 @pytest.mark.parametrize("T", [16, 32, 64, 128])
 @pytest.mark.parametrize("Hq,H", [(1, 1), (8, 1), (6, 2), (16, 1), (11, 1)])
 @pytest.mark.parametrize("D", [64, 128, 256])
-def test_decode_attention(w4, D, Hq, H, T):
+def test_decode_attention(w4, D, Hq, H, T, extra):
     lens = [1, 0, 15, 16, 17, 63, 64, 65, 200, 129, 1000]
     P = 130 if T == 16 else 70
     cache = _random_cache(w4, P, H, T, D, seed=T)
-    table = _table(lens, T, P, seed=2, extra=2)
+    table = _table(lens, T, P, seed=2, extra=extra)
     q = torch.randn((len(lens), Hq, D), generator=torch.Generator().manual_seed(D)).half()
     out = w4.decode_attention_kv8(q.cuda(), cache, _i32(table), _i32(lens))
     assert bool((out[1] == 0).all())
@@ -217,12 +218,10 @@ def test_decode_attention(w4, D, Hq, H, T):
 @pytest.mark.parametrize("B", [1, 5, 20, 75, 150])
 @pytest.mark.parametrize("D,Hq,H,T", [(64, 8, 1, 16), (64, 24, 2, 128), (128, 4, 2, 32), (128, 11, 1, 64), (256, 8, 1, 64), (256, 16, 1, 16)])
 def test_decode_short_tables(w4, D, Hq, H, T, B):
-    # tables of up to 1024 tokens: clusters of 8, 4, 2 and 1 CTAs for each pair,
+    # tables of up to 4096 tokens: clusters of 8, 4, 2 and 1 CTAs for each pair,
     # sequences shorter than a cluster's warps and as long as the table
-    if B * H > 152:
-        B = 152 // H
     rs = np.random.RandomState(B + D)
-    lens = [[1024, 0, 1, 16, 17, 640, 1009, 127, 128, 129][i] if i < 10 else int(rs.randint(0, 400)) for i in range(B)]
+    lens = [[4096, 0, 1, 16, 17, 640, 1009, 127, 128, 129][i] if i < 10 else int(rs.randint(0, 400)) for i in range(B)]
     P = sum(-(-n // T) for n in lens) + 2
     cache = _random_cache(w4, P, H, T, D, seed=T)
     table = _table(lens, T, P, seed=2)
@@ -230,7 +229,7 @@ def test_decode_short_tables(w4, D, Hq, H, T, B):
     out = w4.decode_attention_kv8(q.cuda(), cache, _i32(table), _i32(lens))
     _verify_decode(out, q, cache, table, lens, T)
     # the same tables made longer take the other kernels
-    wide = np.concatenate([table, np.full((B, 1024 // T + 1), -1, np.int32)], 1)
+    wide = np.concatenate([table, np.full((B, 4096 // T + 1), -1, np.int32)], 1)
     other = w4.decode_attention_kv8(q.cuda(), cache, _i32(wide), _i32(lens))
     _verify_decode(other, q, cache, table, lens, T)
     assert w4.get_device_status() == 0
@@ -248,13 +247,14 @@ def test_decode_long_and_short(w4, D, T):
     _verify_decode(out, q, cache, table, lens, T)
 
 
-def test_decode_many_sequences(w4):
+@pytest.mark.parametrize("extra", [0, 300])
+def test_decode_many_sequences(w4, extra):
     rs = np.random.RandomState(5)
     lens = [int(x) for x in rs.randint(0, 40, 700)]
     T, D = 16, 64
     P = sum(-(-n // T) for n in lens) + 1
     cache = _random_cache(w4, P, 1, T, D, seed=7)
-    table = _table(lens, T, P, seed=4)
+    table = _table(lens, T, P, seed=4, extra=extra)
     q = torch.randn((len(lens), 2, D), generator=torch.Generator().manual_seed(1)).half()
     out = w4.decode_attention_kv8(q.cuda(), cache, _i32(table), _i32(lens))
     _verify_decode(out, q, cache, table, lens, T)
@@ -271,12 +271,13 @@ def test_decode_one_long_sequence_equal_to_parts(w4):
     _verify_decode(out, q, cache, table, [n], T)
 
 
-def test_decode_scales_of_every_size(w4):
+@pytest.mark.parametrize("extra", [0, 300])
+def test_decode_scales_of_every_size(w4, extra):
     # blocks whose scales differ by many powers of two, zero scales, equal
     # values everywhere; what is behind a sequence's end holds anything
     T, D, n = 32, 128, 300
     cache = _random_cache(w4, 12, 1, T, D, seed=3)
-    table = _table([n], T, 12, seed=1)
+    table = _table([n], T, 12, seed=1, extra=extra)
     q = torch.randn((1, 8, D), generator=torch.Generator().manual_seed(1)).half()
     rs = np.random.RandomState(2)
     for kmul, vmul in (([1e-4, 1.0], [1e-9, 1e-3, 1.0, 300.0]), ([1.0], [1e-9]), ([0.0, 1.0], [0.0, 1.0]), ([0.5], [0.0])):
@@ -291,10 +292,11 @@ def test_decode_scales_of_every_size(w4):
         _verify_decode(out, q, ref, table, [n], T)
 
 
-def test_decode_growing_scores(w4):
+@pytest.mark.parametrize("extra", [0, 300])
+def test_decode_growing_scores(w4, extra):
     T, D, n = 16, 64, 900
     cache = _random_cache(w4, 60, 1, T, D, seed=3)
-    table = _table([n], T, 60, seed=1)
+    table = _table([n], T, 60, seed=1, extra=extra)
     q = torch.randn((1, 8, D), generator=torch.Generator().manual_seed(1)).half()
     for order in (1, -1):
         for i in range(57):
@@ -304,13 +306,15 @@ def test_decode_growing_scores(w4):
         _verify_decode(out, q, cache, table, [n], T)
 
 
-def test_decode_without_a_page(w4):
+@pytest.mark.parametrize("extra", [0, 300])
+def test_decode_without_a_page(w4, extra):
     # tokens on no page are left out: as if the sequence had the others only
     T, D = 16, 64
     cache = _random_cache(w4, 6, 1, T, D, seed=3)
     q = torch.randn((3, 4, D), generator=torch.Generator().manual_seed(1)).half()
     table = np.array([[0, 1, 2], [0, 99, 2], [-1, 6, -7]], np.int32)
-    out = w4.decode_attention_kv8(q.cuda(), cache, _i32(table), _i32([48, 48, 48]))
+    wide = np.concatenate([table, np.full((3, extra), -9, np.int32)], 1)
+    out = w4.decode_attention_kv8(q.cuda(), cache, _i32(wide), _i32([48, 48, 48]))
     assert w4.get_device_status() == ERR_PAGE
     _verify_decode(out[:1], q[:1], cache, table, [48], T)
     _verify_decode(out[1:2], q[1:2], cache, np.array([[0, 2]]), [32], T)
@@ -517,7 +521,7 @@ def test_refusals(w4):
     with pytest.raises(w4.W4A8Error):
         w4.decode_attention_kv8(q[:, :3].contiguous(), cache, table, lens)
     with pytest.raises(w4.W4A8Error):
-        w4.decode_attention_kv8(q, cache, table.repeat(1, 100), lens, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        w4.decode_attention_kv8(q, cache, table.repeat(1, 200), lens, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ValueError):
         w4.kv8_append(cache, q, q, table, lens, _cu([1]))
     with pytest.raises(TypeError):
