@@ -6,11 +6,14 @@
 // freed by setting its length to 0.  Everything here follows from the table
 // and the lengths alone and has one result: lists are ascending.
 //
-// Held pages are marked in a bitmap that a cluster of 8 CTAs keeps in its
-// shared memory (each CTA an eighth), set through distributed shared memory
-// and counted by prefix sums: one launch with no pass over global memory but
-// the table's own.  Page contents are copied by a kernel of their own over
-// the whole GPU, bound by memory.
+// Held pages are marked in a bitmap in shared memory and counted by prefix
+// sums: one launch with no pass over global memory but the table's own.  One
+// CTA does it where the table and the bitmap are small; else a cluster of 8,
+// each with an eighth of the bitmap, set through distributed shared memory.  (A
+// table of 200 entries: one CTA takes 1 us less than the cluster with its
+// barriers; one of 31k: 20 us against 11, one SM's loads being the limit.)
+// Page contents are copied by a kernel of their own over the whole GPU, bound
+// by memory: 210 MB read and written in 29 us beside a launch, 7.2 TB/s.
 #include "common.cuh"
 #include "kernels.h"
 #include "kv8.cuh"
@@ -20,7 +23,8 @@ namespace {
 
 using namespace w4a8;
 
-constexpr int CL = 8;                            // CTAs of the marking cluster
+constexpr int CLUSTER = 8;                       // CTAs of the marking cluster
+constexpr int kSmallTable = 4096;                // entries that one CTA marks
 constexpr int NT = 1024;
 constexpr int kMapBytes = 192 * 1024;            // bitmap bytes per CTA, at most
 
@@ -56,9 +60,21 @@ __device__ __forceinline__ int scan_block(int v, int *sm, int &before) {
     return total;
 }
 
+template <int CL>
+__device__ __forceinline__ void all_sync() {
+    if (CL == 1) __syncthreads();
+    else cluster_sync_all();
+}
+
 // Sum over the cluster's CTAs of their block totals: (all, those of lower
 // rank).  Each use has its own word *sm, which peers may read until the end.
+template <int CL>
 __device__ __forceinline__ int scan_cluster(int mine, int *sm, int rank, int &before) {
+    if (CL == 1) {
+        before = 0;
+        __syncthreads();
+        return mine;
+    }
     if (threadIdx.x == 0) *sm = mine;
     cluster_sync_all();
     int all = 0;
@@ -74,7 +90,8 @@ __device__ __forceinline__ int scan_cluster(int mine, int *sm, int rank, int &be
 
 __device__ __forceinline__ uint32_t bits_below(long long n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
 
-__global__ void __launch_bounds__(NT) __cluster_dims__(CL, 1, 1) kv8_mark_kernel(const MarkArgs a) {
+template <int CL>
+__global__ void __launch_bounds__(NT) kv8_mark_kernel(const MarkArgs a) {
     extern __shared__ uint32_t map[];            // this CTA's words of the bitmap
     __shared__ int sm_w[NT / 32];
     __shared__ int sm_c[4];
@@ -86,36 +103,42 @@ __global__ void __launch_bounds__(NT) __cluster_dims__(CL, 1, 1) kv8_mark_kernel
     const uint32_t base = smem_u32(map);
     const long long entries = (long long)a.S * a.maxp, step = (long long)CL * NT;
     bool cleared = false;
-    // four entries at a time, their lengths and pages all on the way together
+    // BATCH entries at a time, their lengths and pages all on the way together
     // (entries that do not count are read too: the table has them)
-    for (long long e0 = 0; e0 < entries || !cleared; e0 += 4 * step) {
-        int id[4], len[4], at[4];
+    constexpr int BATCH = 4;
+    for (long long e0 = 0; e0 < entries || !cleared; e0 += BATCH * step) {
+        int id[BATCH], len[BATCH], at[BATCH];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < BATCH; ++k) {
             const long long e = e0 + k * step + (long long)rank * NT + threadIdx.x;
             id[k] = len[k] = at[k] = 0;
             if (e < entries) {
-                const int b = (int)(e / a.maxp);
+                const int b = CL == 1 ? (int)((unsigned)e / (unsigned)a.maxp) : (int)(e / a.maxp);
                 at[k] = (int)(e - (long long)b * a.maxp);
                 len[k] = a.lens[b];
                 id[k] = a.table[e];
             }
         }
-        if (!cleared) cluster_sync_all();        // every CTA's map is clear
+        if (!cleared) all_sync<CL>();            // every CTA's map is clear
         cleared = true;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < BATCH; ++k) {
             if (len[k] <= 0 || at[k] > (len[k] - 1) / a.T) continue;
             if (id[k] < 0 || id[k] >= a.P) {
                 atomicExch(a.status, (int)W4A8_ERR_PAGE);
                 continue;
             }
-            const int w = id[k] >> 5, owner = w / a.words;
-            const uint32_t to = dsmem_addr(base + (uint32_t)(w - owner * a.words) * 4u, (uint32_t)owner);
-            asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(to), "r"(1u << (id[k] & 31)) : "memory");
+            const int w = id[k] >> 5;
+            if (CL == 1) {
+                atomicOr(&map[w], 1u << (id[k] & 31));
+            } else {
+                const int owner = w / a.words;
+                const uint32_t to = dsmem_addr(base + (uint32_t)(w - owner * a.words) * 4u, (uint32_t)owner);
+                asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(to), "r"(1u << (id[k] & 31)) : "memory");
+            }
         }
     }
-    cluster_sync_all();
+    all_sync<CL>();
 
     const long long first = (long long)rank * a.words * 32;      // this CTA's first page
     auto real = [&](int w) { return bits_below((long long)a.P - (first + (long long)w * 32)); };    // real pages of a word
@@ -124,7 +147,7 @@ __global__ void __launch_bounds__(NT) __cluster_dims__(CL, 1, 1) kv8_mark_kernel
         int c = 0, before;
         for (int w = threadIdx.x; w < a.words; w += NT) c += __popc(bits(w));
         const int mine = scan_block(c, sm_w, before);
-        return scan_cluster(mine, sm, rank, skip);
+        return scan_cluster<CL>(mine, sm, rank, skip);
     };
     // act(rank of the page among the counted ones, page), a lane for each page
     auto each = [&](auto bits, int skip, auto act) {
@@ -169,7 +192,7 @@ __global__ void __launch_bounds__(NT) __cluster_dims__(CL, 1, 1) kv8_mark_kernel
             *a.moves = moves;
         }
     }
-    cluster_sync_all();                          // no CTA leaves while a peer may still read its words
+    if (CL > 1) cluster_sync_all();              // no CTA leaves while a peer may still read its words
 }
 
 // ------------------------------------------------------------ page contents
@@ -314,20 +337,45 @@ CopyArgs copy_args(const w4a8_host::Kv8Cache &c) {
     return {{c.k_codes, c.v_codes}, {c.k_scale, c.v_scale}, (long long)c.Hkv * c.T * c.D, c.Hkv * (c.T / kv8::kBlockTokens)};
 }
 
-int map_words(int P) { return (int)(((long long)P + 32 * CL - 1) / (32 * CL)); }
+int map_words(int P, int CL) { return (int)(((long long)P + 32 * CL - 1) / (32 * CL)); }
+
+template <int CL>
+w4a8_status launch_mark_n(MarkArgs a, cudaStream_t stream) {
+    static std::atomic<int> attr_done[w4a8_host::kDeviceSlots];
+    const w4a8_status st = w4a8_host::ensure_smem_limit(kv8_mark_kernel<CL>, kMapBytes, attr_done);
+    if (st != W4A8_OK) return st;
+    a.words = map_words(a.P, CL);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(CL);
+    cfg.blockDim = dim3(NT);
+    cfg.dynamicSmemBytes = (size_t)a.words * 4;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CL;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CL > 1 ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, kv8_mark_kernel<CL>, a) != cudaSuccess) {
+        cudaGetLastError();
+        return W4A8_ERR_CUDA;
+    }
+    return w4a8_host::launch_status();
+}
 
 w4a8_status launch_mark(const MarkArgs &a, cudaStream_t stream) {
-    static std::atomic<int> attr_done[w4a8_host::kDeviceSlots];
-    const w4a8_status st = w4a8_host::ensure_smem_limit(kv8_mark_kernel, kMapBytes, attr_done);
-    if (st != W4A8_OK) return st;
-    return w4a8_host::launch_dependent(kv8_mark_kernel, dim3(CL), NT, (size_t)a.words * 4, stream, a);
+    const bool small = (long long)a.S * a.maxp <= kSmallTable && (long long)map_words(a.P, 1) * 4 <= kMapBytes / 8;
+    return small ? launch_mark_n<1>(a, stream) : launch_mark_n<CLUSTER>(a, stream);
 }
 
 }  // namespace
 
 namespace w4a8_host {
 
-bool kv8_pages_supported(int P) { return (long long)map_words(P) * 4 <= kMapBytes; }
+bool kv8_pages_supported(int P) { return (long long)map_words(P, CLUSTER) * 4 <= kMapBytes; }
 
 // holes [P / 2 + 1], movers [P / 2 + 1], remap [P], moves [1]
 size_t kv8_compact_workspace_bytes(int P) { return ((size_t)P + 2 * ((size_t)P / 2 + 1) + 1) * 4; }
@@ -341,7 +389,6 @@ w4a8_status launch_kv8_free_pages(const int32_t *table, const int32_t *lens, int
     a.maxp = maxp;
     a.T = T;
     a.P = P;
-    a.words = map_words(P);
     a.ids = ids;
     a.count = count;
     a.status = device_status_ptr();
@@ -360,7 +407,6 @@ w4a8_status launch_kv8_compact(const Kv8Cache &c, const int32_t *table, const in
     a.maxp = maxp;
     a.T = c.T;
     a.P = c.P;
-    a.words = map_words(c.P);
     a.holes = ws;
     a.movers = ws + half;
     a.remap = ws + 2 * half;
