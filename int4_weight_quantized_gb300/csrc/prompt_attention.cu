@@ -204,7 +204,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
     if (threadIdx.x < 16) sm_bad[threadIdx.x >> 2][threadIdx.x & 3] = 0u;
     if (threadIdx.x == 0) sm_any = 0u;
     constexpr int W_TMA = 4 * C::GROUPS, W_MMA = W_TMA + 1;
-    if (threadIdx.x == 0) {
+    if (warp == W_TMA && lane == 0) {                        // the thread that copies: it need not wait for another
         for (int i = 0; i < C::NQ; ++i) mbar_init(&qbar[i], 1);
         for (int i = 0; i < C::NS; ++i) {
             mbar_init(&sbar[i], 1);
@@ -224,6 +224,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         *abort_flag = 0u;
         fence_barrier_init();
     }
+    __syncwarp();
     if (warp == W_TMA && lane < 3) prefetch_map(lane == 0 ? &tm_q : lane == 1 ? &tm_k : &tm_v);
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
@@ -243,6 +244,27 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         nmax = max(nmax, steps_of[i]);
     }
 
+    auto load_slot = [&](const CUtensorMap *tm, int step, int h, int slot) {
+        mbar_arrive_expect_tx(&full[slot], C::SLOT);
+#pragma unroll
+        for (int c = 0; c < C::SD / 64; ++c)
+            tma_load_3d(sbase + C::OFF_RING + slot * C::SLOT + c * (BN * 128), tm, h * C::SD + c * 64, head, job.k0 + step * BN,
+                        smem_u32(&full[slot]));
+    };
+    auto load_q = [&](int i) {
+        mbar_arrive_expect_tx(&qbar[i], (uint32_t)(a.tok * a.G * D * 2));
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+            tma_load_3d(sbase + i * C::QTILE + c * (128 * 128), &tm_q, c * 64, head * a.G, job.q0 + job.t0 + i * a.tok, smem_u32(&qbar[i]));
+    };
+    // the first tiles are on their way while the others get ready
+    if (warp == W_TMA && lane == 0 && nmax > 0) {
+        load_q(0);
+#pragma unroll
+        for (int h = 0; h < C::SPT; ++h) load_slot(&tm_k, 0, h, h);
+    }
+    __syncwarp();
+
     // Tensor memory is taken after the kernel before this one has ended and
     // before the next one may begin: two kernels on an SM that each hold some
     // while waiting for the other would wait forever.
@@ -256,7 +278,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
 
     if (warp == W_TMA) {
         if (lane == 0 && nmax > 0) {
-            int slot = 0;
+            int slot = C::SPT;
             uint32_t phase = 0;
             bool ok = true;
             auto load_tile = [&](const CUtensorMap *tm, int step) {
@@ -264,26 +286,13 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                 for (int h = 0; h < C::SPT; ++h) {
                     ok = ok && wait(&empty[slot], phase ^ 1u);
                     if (!ok) return;
-                    mbar_arrive_expect_tx(&full[slot], C::SLOT);
-#pragma unroll
-                    for (int c = 0; c < C::SD / 64; ++c)
-                        tma_load_3d(sbase + C::OFF_RING + slot * C::SLOT + c * (BN * 128), tm, h * C::SD + c * 64, head,
-                                    job.k0 + step * BN, smem_u32(&full[slot]));
+                    load_slot(tm, step, h, slot);
                     if (++slot == C::NSLOT) {
                         slot = 0;
                         phase ^= 1u;
                     }
                 }
             };
-            auto load_q = [&](int i) {
-                mbar_arrive_expect_tx(&qbar[i], (uint32_t)(a.tok * a.G * D * 2));
-#pragma unroll
-                for (int c = 0; c < D / 64; ++c)
-                    tma_load_3d(sbase + i * C::QTILE + c * (128 * 128), &tm_q, c * 64, head * a.G,
-                                job.q0 + job.t0 + i * a.tok, smem_u32(&qbar[i]));
-            };
-            load_q(0);
-            load_tile(&tm_k, 0);
             for (int i = 1; i < C::NQ; ++i) load_q(i);
             for (int j = 0; j < nmax; ++j) {
                 if (C::K_FIRST && j + 1 < nmax) load_tile(&tm_k, j + 1);

@@ -362,12 +362,13 @@ def _held(table, lens, T):
     return sorted({int(p) for row, n in zip(table, lens) for p in row[:-(-n // T)]})
 
 
+@pytest.mark.parametrize("extra", [0, 5000])
 @pytest.mark.parametrize("P", [1, 31, 32, 33, 255, 256, 257, 5000, 300001])
-def test_free_pages(w4, P):
+def test_free_pages(w4, P, extra):
     T = 16
     rs = np.random.RandomState(P)
     lens = [int(x) for x in rs.randint(0, 5 * T, 12)] if P > 100 else [min(P, 3) * T - 5, 0]
-    table = _table(lens, T, P, seed=P)
+    table = _table(lens, T, P, seed=P, extra=extra)
     cache = w4.kv8_cache(P, 1, T, 64)
     ids, count = w4.kv8_free_pages(cache, _i32(table), _i32(lens))
     want = sorted(set(range(P)) - set(_held(table, lens, T)))
@@ -418,15 +419,16 @@ def test_fork_refuses_bad_places(w4):
         assert np.array_equal(a, b)
 
 
+@pytest.mark.parametrize("extra", [2, 5000])       # tables of either kind of marking
 @pytest.mark.parametrize("P,T,H,D", [(9, 16, 1, 64), (64, 32, 2, 128), (257, 16, 3, 64), (3000, 16, 1, 64), (40, 128, 2, 256)])
-def test_compact(w4, P, T, H, D):
+def test_compact(w4, P, T, H, D, extra):
     rs = np.random.RandomState(P)
     lens, left = [], int(P * 0.6)
     while left > 0 and len(lens) < 30:
         n = int(rs.randint(0, min(left, 40) + 1))
         lens.append(max(0, n * T - int(rs.randint(0, T))))
         left -= n
-    table = _table(lens, T, P, seed=P, extra=2)
+    table = _table(lens, T, P, seed=P, extra=extra)
     if len(lens) > 1 and lens[0] > 0:                 # a shared page
         other = int(np.argmax(lens[1:])) + 1
         if lens[other] >= T and lens[0] >= T:
