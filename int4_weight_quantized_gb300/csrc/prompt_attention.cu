@@ -473,7 +473,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                 w = w && wait.warp(&full[slot], (uint32_t)(at / C::NSLOT) & 1u);
                 if (!w) return false;
                 const uint8_t *row = smem + C::OFF_RING + slot * C::SLOT + r * 128;
-#pragma unroll
+#pragma unroll 4
                 for (int c = 0; c < C::SD / 8; ++c) {
                     // (the order differs by lane: no two of 8 lanes meet in a bank)
                     const uint4 x = *reinterpret_cast<const uint4 *>(row + (c >> 3) * (BN * 128) + ((c + r) & 7) * 16);
@@ -566,7 +566,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                     ok = wait.warp(&obar[grp], (uint32_t)(j - 1) & 1u);
                     if (!ok) break;
                     tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < D / 16; ++c) {
                         uint32_t v[16];
                         tmem_ld_cols<16>(ocol + (uint32_t)(c * 16), v);
@@ -629,7 +629,13 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         const bool mine = r < a.tok * a.G && tok_i < job.nq;
         uint16_t *dst = a.out + ((size_t)(job.q0 + tok_i) * a.Hq + (size_t)head * a.G + r % a.G) * D;
         const float inv = l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l);
-#pragma unroll
+        // Out through shared memory, in the place of this tile's Q (a tile without
+        // steps has not waited for it): a row of 16-byte stores to each lane would
+        // touch 32 lines an instruction (2.4 us of an 11 us call at D = 256, 0.9 so).
+        // The 16-byte pieces of a row are permuted by the row against conflicts.
+        if (steps == 0 && nmax > 0) ok = ok && wait.warp(&qbar[grp], 0);
+        uint8_t *stage = smem + grp * C::QTILE + w4 * (32 * D * 2);
+#pragma unroll 1                                             // code that runs once is fetched once: small is fast
         for (int c = 0; c < D / 32; ++c) {
             uint32_t v[32];
 #pragma unroll
@@ -638,19 +644,28 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                 tmem_ld_cols<32>(ocol + (uint32_t)(c * 32), v);
                 tmem_ld_wait();
             }
-            if (mine && (ok || steps == 0)) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    uint32_t w[4];
+            for (int e = 0; e < 4; ++e) {
+                uint32_t w[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const __half2 h = __floats2half2_rn(__uint_as_float(v[8 * e + 2 * k]) * inv, __uint_as_float(v[8 * e + 2 * k + 1]) * inv);
-                        w[k] = *reinterpret_cast<const uint32_t *>(&h);
-                    }
-                    *reinterpret_cast<uint4 *>(dst + 32 * c + 8 * e) = make_uint4(w[0], w[1], w[2], w[3]);
+                for (int k = 0; k < 4; ++k) {
+                    const __half2 h = __floats2half2_rn(__uint_as_float(v[8 * e + 2 * k]) * inv, __uint_as_float(v[8 * e + 2 * k + 1]) * inv);
+                    w[k] = *reinterpret_cast<const uint32_t *>(&h);
                 }
+                *reinterpret_cast<uint4 *>(stage + lane * (D * 2) + (((4 * c + e) ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
             }
         }
+        __syncwarp();
+        const uint32_t rows = __ballot_sync(0xffffffffu, mine && ok);
+        constexpr int LPR = D / 8, RPI = 32 / LPR;           // lanes to a row, rows an instruction
+#pragma unroll 4
+        for (int i = 0; i < 32 / RPI; ++i) {
+            const int row = i * RPI + lane / LPR, piece = lane % LPR;
+            const size_t to = (size_t)__shfl_sync(0xffffffffu, (unsigned long long)(dst - a.out), row);
+            const uint4 x = *reinterpret_cast<const uint4 *>(stage + row * (D * 2) + ((piece ^ (row & 7)) << 4));
+            if (rows >> row & 1u) *reinterpret_cast<uint4 *>(a.out + to + 8 * piece) = x;
+        }
+        __syncwarp();
         if (*(volatile uint32_t *)&sm_any && mine) {
             // noted keys that this row sees (none, as a rule)
             const volatile uint32_t *noted = &sm_bad[0][0];
