@@ -636,29 +636,30 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         if (steps == 0 && nmax > 0) ok = ok && wait.warp(&qbar[grp], 0);
         uint8_t *stage = smem + grp * C::QTILE + w4 * (32 * D * 2);
 #pragma unroll 1                                             // code that runs once is fetched once: small is fast
-        for (int c = 0; c < D / 32; ++c) {
-            uint32_t v[32];
+        for (int c = 0; c < D / 64; ++c) {
+            uint32_t v[64];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = 0u;
+            for (int e = 0; e < 64; ++e) v[e] = 0u;
             if (steps > 0 && ok) {
-                tmem_ld_cols<32>(ocol + (uint32_t)(c * 32), v);
+                tmem_ld_cols<32>(ocol + (uint32_t)(c * 64), v);
+                tmem_ld_cols<32>(ocol + (uint32_t)(c * 64 + 32), v + 32);
                 tmem_ld_wait();
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < 8; ++e) {
                 uint32_t w[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const __half2 h = __floats2half2_rn(__uint_as_float(v[8 * e + 2 * k]) * inv, __uint_as_float(v[8 * e + 2 * k + 1]) * inv);
                     w[k] = *reinterpret_cast<const uint32_t *>(&h);
                 }
-                *reinterpret_cast<uint4 *>(stage + lane * (D * 2) + (((4 * c + e) ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                *reinterpret_cast<uint4 *>(stage + lane * (D * 2) + (((8 * c + e) ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
             }
         }
         __syncwarp();
         const uint32_t rows = __ballot_sync(0xffffffffu, mine && ok);
         constexpr int LPR = D / 8, RPI = 32 / LPR;           // lanes to a row, rows an instruction
-#pragma unroll 4
+#pragma unroll 8
         for (int i = 0; i < 32 / RPI; ++i) {
             const int row = i * RPI + lane / LPR, piece = lane % LPR;
             const size_t to = (size_t)__shfl_sync(0xffffffffu, (unsigned long long)(dst - a.out), row);
