@@ -16,7 +16,7 @@
 // They move each byte once; what bounds them is memory at large sizes and
 // the launch with its chain of dependent loads (lengths, table, rows) at
 // small ones.  9 prompts of up to 2500 tokens at 8 heads of 128: 101 MB
-// written in 28 us, with an IEEE division per value 66; 26k tokens read back,
+// written in 25 us, with an IEEE division per value 66; 26k tokens read back,
 // 160 MB, in 30 us; one token of each of 32 sequences 5 us, 3 of them the launch.
 #include "common.cuh"
 #include "kernels.h"
@@ -32,23 +32,19 @@ constexpr int WARPS = 4;
 // is certain: t = fl(x r) and the quotient fl(x / s) are both within 2^-23
 // (relative) of x / s, |x / s| <= 127 (1 + 2^-23), so they differ by less than
 // 2.3e-5 < 2^-15; where t is 2^-14 or more from every half-integer, no rounding
-// border lies between them.  The others (and whatever is not finite) are
-// divided.  1.5 * 2^23 added to t leaves rint(t) in the low bits.
-__device__ __forceinline__ uint2 codes8(uint4 x, float s, float r) {
+// border lies between them.  The others (and whatever is not finite) are named
+// in `near`, a bit each, to be divided.  1.5 * 2^23 added to t leaves rint(t) in
+// the low bits.
+__device__ __forceinline__ uint2 codes8(uint4 x, float r, uint32_t &near) {
     const __half2 *h = reinterpret_cast<const __half2 *>(&x);
     uint32_t q[8];
-    unsigned near = 0u;
+    near = 0u;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         const float f = e & 1 ? __high2float(h[e / 2]) : __low2float(h[e / 2]);
         const float t = f * r, m = t + kMagic;
         if (!(fabsf(t - (m - kMagic)) <= 0.5f - 0x1p-14f)) near |= 1u << e;
         q[e] = __float_as_uint(m);
-    }
-    if (near) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (near & (1u << e)) q[e] = (uint32_t)act_code(e & 1 ? __high2float(h[e / 2]) : __low2float(h[e / 2]), s);
     }
     const uint32_t a = __byte_perm(q[0], q[1], 0x0040), b = __byte_perm(q[2], q[3], 0x0040);
     const uint32_t c = __byte_perm(q[4], q[5], 0x0040), d = __byte_perm(q[6], q[7], 0x0040);
@@ -119,6 +115,7 @@ __global__ void __launch_bounds__(WARPS * 32, D == 64 ? 10 : D == 128 ? 8 : 5) k
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     const float s = fmaxf(s_old, __fdiv_rn(amax, 127.0f));
     const float recip = __fdiv_rn(1.0f, s);
+    uint32_t exact[(NP + 3) / 4] = {};           // a bit for each value that has to be divided
     const bool again = lo > 0 && s > s_old;        // earlier codes of the block change
     const float f_old = again ? __fdiv_rn(s_old, s) : 1.0f;
 #pragma unroll
@@ -126,7 +123,10 @@ __global__ void __launch_bounds__(WARPS * 32, D == 64 ? 10 : D == 128 ? 8 : 5) k
         const int t = i * RPP + row;
         uint32_t *dst = reinterpret_cast<uint32_t *>(cp + (size_t)t * D);
         if (t >= lo && t < hi) {
-            *reinterpret_cast<uint2 *>(dst) = s > 0.0f ? codes8(v[i], s, recip) : make_uint2(0u, 0u);
+            uint32_t near;
+            const uint2 q = codes8(v[i], recip, near);
+            *reinterpret_cast<uint2 *>(dst) = s > 0.0f ? q : make_uint2(0u, 0u);
+            if (s > 0.0f) exact[i / 4] |= near << (8 * (i % 4));
         } else if (t < lo && again) {
             const uint2 w = *reinterpret_cast<const uint2 *>(dst);
             uint32_t u[2] = {w.x, w.y};
@@ -140,6 +140,15 @@ __global__ void __launch_bounds__(WARPS * 32, D == 64 ? 10 : D == 128 ? 8 : 5) k
             *reinterpret_cast<uint2 *>(dst) = make_uint2(u[0], u[1]);
         }
     }
+    // one value in several thousand, each read again: this code is there once
+#pragma unroll
+    for (int k = 0; k < (NP + 3) / 4; ++k)
+        while (exact[k]) {
+            const int bit = __ffs(exact[k]) - 1, t = (4 * k + (bit >> 3)) * RPP + row;
+            exact[k] &= exact[k] - 1;
+            const float f = __half2float(__ushort_as_half(x[(size_t)(r.first + (tok0 + t - start)) * (size_t)ld + (bit & 7)]));
+            cp[(size_t)t * D + (bit & 7)] = (int8_t)act_code(f, s);
+        }
     if (lane == 0) *sp = s;
 }
 
