@@ -12,17 +12,27 @@
 // Rows.  The G = Hq / Hkv query heads of a KV head share its keys, so the 128
 // rows of a tile are floor(128 / G) tokens x G heads (row = token G + head):
 // a short prompt or a chunk fills tiles that one head alone would leave
-// empty, and K and V are read once for the group.  A CTA takes NQ such tiles
-// of consecutive tokens (two for D <= 128, one for D = 256) through all their
-// keys in steps of 128.
+// empty, and K and V are read once for the group.  A CTA takes one or two such
+// tiles of consecutive tokens through all their keys in steps of 128.
 //
-// Roles (one CTA per SM): one thread copies Q, then K and V tiles by TMA into
-// a ring of slots; one warp issues the products, S = Q K^T into tensor memory
-// and O += P V with P taken from tensor memory; 4 warps per S buffer do the
-// softmax, a thread holding one row: maximum, 2^x, sum, and P as fp16 written
-// over S.  With two tiles the tensor cores work on one while the other's
-// softmax runs; with one (D = 256) S has two buffers and the next S is
-// computed ahead.  O stays in tensor memory for the whole pass; it is rescaled
+// Roles: one thread copies Q, then K and V tiles by TMA into a ring of slots;
+// one warp issues the products, S = Q K^T into tensor memory and O += P V with
+// P taken from tensor memory; 4 warps per row tile do the softmax, a thread
+// holding one row: maximum, 2^x, sum, and P as fp16.  What overlaps, and what
+// tensor memory's 512 columns hold, goes by D:
+//   128: two tiles per CTA; the tensor cores work on one while the other's
+//        softmax runs; P lies over its S.  16384 tokens, 16 heads on 2: 669 us,
+//        1640 TFLOP/s; the softmax of a tile takes 1100 cycles beside the 1024
+//        of its two products, and power sets the clock.
+//   256: one tile, S twice: the next S is computed ahead.  8192 tokens, 8 heads
+//        on 1: 1627 TFLOP/s under ncu.
+//   64:  one tile, two CTAs per SM, P beside S: the next S waits only until
+//        this one has been read.  The softmax sets the pace (1030 cycles per
+//        tile and SM beside 512 of products and 512 of the 2^x pipe): 12
+//        sequences of 93-2500 tokens, 24 heads on 8, 111 us.
+// (8 warps per tile, two threads to a row, were slower: 132 us and, at D = 128,
+// 817: what issues the products shares a quarter of the SM with them.)
+// O stays in tensor memory for the whole pass; it is rescaled
 // only when a row's maximum has grown by more than 2^8 since the one in use
 // (p then stays below 2^9, well inside fp16; the final division by the sum of
 // the same p makes the choice of m exact), which after the first tiles is
@@ -631,8 +641,8 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         const float inv = l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l);
         // Out through shared memory, in the place of this tile's Q (a tile without
         // steps has not waited for it): a row of 16-byte stores to each lane would
-        // touch 32 lines an instruction (2.4 us of an 11 us call at D = 256, 0.9 so).
-        // The 16-byte pieces of a row are permuted by the row against conflicts.
+        // touch 32 lines an instruction.  The 16-byte pieces of a row are permuted by
+        // the row against conflicts.
         if (steps == 0 && nmax > 0) ok = ok && wait.warp(&qbar[grp], 0);
         uint8_t *stage = smem + grp * C::QTILE + w4 * (32 * D * 2);
 #pragma unroll 1                                             // code that runs once is fetched once: small is fast
