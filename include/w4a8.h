@@ -310,7 +310,9 @@ w4a8_status w4a8_kv8_read(const w4a8_kv8 *cache, const int32_t *table, const int
  * Tokens on no page are left out.  Requires Hq % heads == 0, Hq/heads <= 16,
  * B <= 65535, max_pages * page_tokens < 2^31, scale finite and > 0, and a
  * workspace of w4a8_decode_attention_kv8_workspace_bytes (0 for an invalid
- * shape; it does not grow with the length). */
+ * shape, and for tables of up to 4096 tokens, which one launch with a cluster
+ * per sequence and KV head takes; above, the sequences are cut over the whole
+ * GPU, and the workspace grows with neither their number nor their length). */
 size_t w4a8_decode_attention_kv8_workspace_bytes(int B, int Hq, int Hkv, int D, int page_tokens, int max_pages);
 w4a8_status w4a8_decode_attention_kv8(const uint16_t *q, const w4a8_kv8 *cache, const int32_t *table,
                                       const int32_t *lens, int B, int Hq, int max_pages, float scale, uint16_t *out,

@@ -425,11 +425,12 @@ __global__ void __launch_bounds__(W * 32, D == 256 || NT == 2 ? 1 : 2) kv8_decod
     const long long U = block_scan(mine, sm_part, before) * a.Hkv;
     sm_scan[threadIdx.x] = before * a.Hkv;
     __syncthreads();
-    // this warp's range; neighbours in the order are on different SMs.  A worker
-    // for each unit up to 512 (a short step wants them all at once), then one
-    // for 4 units until every warp has work: parts cost a read and a write, and a
-    // ring is full with 3 blocks (one sequence of 131072 tokens: 36 us a call
-    // with a worker per unit, 29 so)
+    // This warp's range; neighbours in the order are on different SMs.  A worker
+    // for each unit up to 512 (a short step wants them all at once), then one for
+    // 4 units until every warp has work: parts cost a read and a write, but a
+    // warp's blocks follow one another.  One sequence of 131072 tokens, 2 KV heads
+    // of 128, us on the device: a worker for each unit 36, for 2 31, for 4 29, for
+    // 6 37; 8 of 8192 tokens, 1 head: for 2 23, for 4 27, for 6 27.
     const long long C = min((long long)gridDim.x * W, max(min(U, 512LL), U / 4)), c = (long long)warp * gridDim.x + blockIdx.x;
     if (c >= C) return;
     const long long u0 = kv8::first_unit(c, U, C), u1 = kv8::first_unit(c + 1, U, C);
