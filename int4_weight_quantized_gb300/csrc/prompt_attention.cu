@@ -60,6 +60,7 @@ namespace {
 using namespace w4a8;
 
 constexpr int BN = 128;              // keys per step
+constexpr long long kDrain = 1LL << 31;   // cycles that a CTA which gives up waits for what it has under way
 
 template <int D>
 struct Cfg {
@@ -310,9 +311,9 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                 if (!C::K_FIRST && j + 1 < nmax) load_tile(&tm_k, j + 1);
             }
             // no copy is in flight when the CTA leaves: Q's, and every slot's last
-            for (int i = 0; i < C::NQ; ++i) mbar_wait_bounded(&qbar[i], 0, a.budget, a.status);
+            for (int i = 0; i < C::NQ; ++i) mbar_wait_bounded(&qbar[i], 0, kDrain, a.status);
             if (!ok)
-                for (int i = 0; i < C::NSLOT; ++i) mbar_wait_bounded(&full[i], i < slot ? phase : phase ^ 1u, a.budget, a.status);
+                for (int i = 0; i < C::NSLOT; ++i) mbar_wait_bounded(&full[i], i < slot ? phase : phase ^ 1u, kDrain, a.status);
         }
     } else if (warp == W_MMA) {
         // One lane issues everything; the whole warp walks the ring with it, so
@@ -446,7 +447,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
                 if (!ok) {
                     // a wait ran out: what was issued still has to end before the CTA leaves
                     tc_commit_if(one, bar_at(drain));
-                    mbar_wait_bounded(drain, 0, a.budget, a.status);
+                    mbar_wait_bounded(drain, 0, kDrain, a.status);
                 }
             }
         }
