@@ -312,7 +312,7 @@ w4a8_status w4a8_kv8_read(const w4a8_kv8 *cache, const int32_t *table, const int
  * workspace of w4a8_decode_attention_kv8_workspace_bytes (0 for an invalid
  * shape, and for tables of up to 4096 tokens, which one launch with a cluster
  * per sequence and KV head takes; above, the sequences are cut over the whole
- * GPU, and the workspace grows with neither their number nor their length). */
+ * GPU, and the workspace does not grow with their length). */
 size_t w4a8_decode_attention_kv8_workspace_bytes(int B, int Hq, int Hkv, int D, int page_tokens, int max_pages);
 w4a8_status w4a8_decode_attention_kv8(const uint16_t *q, const w4a8_kv8 *cache, const int32_t *table,
                                       const int32_t *lens, int B, int Hq, int max_pages, float scale, uint16_t *out,

@@ -43,9 +43,7 @@ __device__ __forceinline__ int find_sequence(const int32_t *cu, int B, int total
 // The page that holds a sequence's page-th T tokens; -1 when the table has no
 // such entry or names no page of the cache.
 __device__ __forceinline__ int page_at(const int32_t *table, int b, int maxp, int page, int P) {
-    if (page >= maxp) return -1;
-    const int id = table[(size_t)b * maxp + page];
-    return id >= 0 && id < P ? id : -1;
+    return page_of_row(table + (size_t)b * maxp, maxp, page, P);
 }
 
 }  // namespace kv8

@@ -29,6 +29,19 @@ KV8_FN size_t scale_offset(int page, int Hkv, int head, int T, int tok) {
     return ((size_t)page * Hkv + head) * (size_t)(T / kBlockTokens) + tok / kBlockTokens;
 }
 
+// What a table may name: a page of the cache's P, or none (-1): an entry behind
+// the table's row end, or one that names no page, is none.
+KV8_FN int valid_page(int id, int P) { return id >= 0 && id < P ? id : -1; }
+KV8_FN int page_of_row(const int32_t *row, int maxp, int page, int P) {
+    return page >= 0 && page < maxp ? valid_page(row[page], P) : -1;
+}
+// Entries of a row that count: those that hold its first len tokens (none for
+// len <= 0), never more than the row has.
+KV8_FN int held_entries(int len, int T, int maxp) {
+    const int n = len <= 0 ? 0 : (len - 1) / T + 1;
+    return n < maxp ? n : maxp;
+}
+
 // Packed sequences: sequence b has rows cu[b] .. cu[b+1] - 1.  Work items of
 // `unit` rows are numbered without a pass over all lengths: sequence b's
 // items begin at cu[b] / unit + slack * b.  That leaves it at least

@@ -123,8 +123,8 @@ __global__ void __launch_bounds__(NT) kv8_mark_kernel(const MarkArgs a) {
         cleared = true;
 #pragma unroll
         for (int k = 0; k < BATCH; ++k) {
-            if (len[k] <= 0 || at[k] > (len[k] - 1) / a.T) continue;
-            if (id[k] < 0 || id[k] >= a.P) {
+            if (at[k] >= kv8::held_entries(len[k], a.T, a.maxp)) continue;
+            if (kv8::valid_page(id[k], a.P) < 0) {
                 atomicExch(a.status, (int)W4A8_ERR_PAGE);
                 continue;
             }
@@ -283,10 +283,9 @@ __global__ void __launch_bounds__(CT, 6) kv8_compact_kernel(const CompactArgs a)
         const int b = (int)(e / a.maxp), i = (int)(e - (long long)b * a.maxp);
         const int len = a.lens[b];
         int id = -1;
-        if (len > 0 && i <= (len - 1) / a.T) {
-            id = a.table[e];
-            if (id < 0 || id >= a.P) id = -1;
-            else if (id >= n) id = a.remap[id];
+        if (i < kv8::held_entries(len, a.T, a.maxp)) {
+            id = kv8::valid_page(a.table[e], a.P);
+            if (id >= n) id = a.remap[id];
         }
         a.table_out[e] = id;
     }
@@ -318,7 +317,7 @@ __global__ void __launch_bounds__(CT) kv8_fork_kernel(const ForkArgs a) {
     if (ok && part) {
         from = kv8::page_at(a.table, src, a.maxp, np - 1, a.P);
         to = a.fresh[i];
-        ok = from >= 0 && to >= 0 && to < a.P;
+        ok = from >= 0 && kv8::valid_page(to, a.P) >= 0;
     }
     if (!ok) {
         if (blockIdx.x == 0 && threadIdx.x == 0) atomicExch(a.status, (int)W4A8_ERR_PAGE);

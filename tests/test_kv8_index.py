@@ -34,6 +34,21 @@ def test_offsets_pass_32_bits(X):
     assert X.scale_offset(300000000, 8, 7, 128, 127) == (300000000 * 8 + 7) * 8 + 7
 
 
+def test_bad_pages_are_none(X):
+    lo, hi = -2 ** 31, 2 ** 31 - 1
+    row = (ctypes.c_int32 * 6)(0, 9, 10, -1, lo, hi)
+    assert [X.page_of_row(row, 6, i, 10) for i in range(6)] == [0, 9, -1, -1, -1, -1]
+    assert X.page_of_row(row, 6, 5, hi) == -1 and X.page_of_row(row, 6, 2, hi) == 10
+    # behind the row's end nothing is read
+    assert [X.page_of_row(row, n, i, 10) for n, i in ((0, 0), (1, 1), (6, 6), (6, hi), (6, -1), (6, lo))] == [-1] * 6
+
+
+def test_held_entries(X):
+    for T in (16, 32, 64, 128):
+        assert [X.held_entries(n, T, 5) for n in (-2 ** 31, -1, 0, 1, T, T + 1, 4 * T, 5 * T, 5 * T + 1, 2 ** 31 - 1)] == \
+            [0, 0, 0, 1, 1, 2, 4, 5, 5, 5]
+
+
 @pytest.mark.parametrize("unit,slack", [(16, 1), (16, 2), (1, 1), (8, 1), (42, 1), (256, 1)])
 def test_items_reach_every_row_once(X, unit, slack):
     rng = random.Random(unit * 10 + slack)
