@@ -6,13 +6,14 @@
 // sequence, so every cached byte is read once and used for the Hq / Hkv heads
 // of its group: the bytes of the cache are the time.
 //
-// Split.  The (sequence, KV head) pairs' 64-token tiles are numbered in order
+// Split.  The (sequence, KV head) pairs' 32-token tiles are numbered in order
 // and cut into equal ranges, one per warp, wherever the cuts fall: long and
 // short sequences balance, one long sequence spreads over the whole GPU, and
 // no warp waits for another.  A warp's range is a run of segments (one per
 // pair); a segment that is a whole pair is written out, the first and the last
 // may be parts of one and go to the workspace (two slots per warp) for the
-// combine kernel.
+// combine kernel.  Where pairs are few and long, a CTA whose ranges are inside
+// one pair joins its warps' parts in shared memory first.
 //
 // Tiles.  A warp takes 16 tokens (one scale block) at a time.  Its own ring of
 // asynchronous copies in shared memory keeps the next blocks' K, V and scales
@@ -51,7 +52,7 @@ namespace {
 using namespace w4a8;
 
 constexpr int W = 8;                 // warps per CTA
-constexpr int TILE = 64;             // tokens per unit of the split
+constexpr int TILE = 32;             // tokens per unit of the split
 constexpr int MAXC = 152 * 2;        // CTAs at most
 constexpr int MAXW = MAXC * W;       // workers (warps) at most
 constexpr int PAIR_TOKENS = 4096;    // tokens that a table may hold for the pair kernel
@@ -405,8 +406,11 @@ template <int D, int NT>
 __global__ void __launch_bounds__(W * 32, D == 256 || NT == 2 ? 1 : 2) kv8_decode_kernel(const DecodeArgs a) {
     using R = Ring<D>;
     constexpr int NJ = D / 16;            // product tiles of 16 d
-    extern __shared__ __align__(128) uint8_t smem[];         // the warps' rings
+    constexpr int NH = 8 * NT, LD = D + 4;                   // a head's row in shared memory, padded against bank conflicts
+    static_assert(W * NH * LD * 4 <= R::BYTES, "the warps' O fits the rings");
+    extern __shared__ __align__(128) uint8_t smem[];         // the warps' rings; at the end their O
     __shared__ float sm_sc[W][R::S][2];
+    __shared__ float2 sm_ml[W][8 * NT];
     __shared__ long long sm_scan[W * 32];
     __shared__ long long sm_part[W];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -425,13 +429,20 @@ __global__ void __launch_bounds__(W * 32, D == 256 || NT == 2 ? 1 : 2) kv8_decod
     const long long U = block_scan(mine, sm_part, before) * a.Hkv;
     sm_scan[threadIdx.x] = before * a.Hkv;
     __syncthreads();
-    // This warp's range; neighbours in the order are on different SMs.  A worker
-    // for each unit up to 512 (a short step wants them all at once), then one for
-    // 4 units until every warp has work: parts cost a read and a write, but a
-    // warp's blocks follow one another.  One sequence of 131072 tokens, 2 KV heads
-    // of 128, us on the device: a worker for each unit 36, for 2 31, for 4 29, for
-    // 6 37; 8 of 8192 tokens, 1 head: for 2 23, for 4 27, for 6 27.
-    const long long C = min((long long)gridDim.x * W, max(min(U, 512LL), U / 4)), c = (long long)warp * gridDim.x + blockIdx.x;
+    // This warp's range.  Where there are 2 W workers or more to a pair, every warp
+    // works (a worker for each unit at most), a CTA's warps are neighbours in the
+    // order, and those of a CTA inside one pair join their parts on chip; a part
+    // from every warp would make the merge dearer than what the warps save (a
+    // worker for 4 units was best then).  us a call, so / with a part from every
+    // warp: one sequence of 131072 tokens, 2 KV heads of 128, 23.0 / 25.7; 4 of
+    // 32768 22.2 / 26.2; 8 of 8192, 1 head, 13.1 / 17.6; 4 of 16384, 8 heads,
+    // 32.0 / 34.2; with units of 64 tokens 24.0, 25.4, 17.5 and 33.9.
+    // Otherwise neighbours in the order are on different SMs, and there is a worker
+    // for each unit up to 512 and then one for 256 tokens until every warp has work.
+    const long long all = min((long long)gridDim.x * W, U) / W * W;
+    const bool groups = all >= 2LL * W * a.B * a.Hkv;
+    const long long C = groups ? all : min((long long)gridDim.x * W, max(min((U * TILE + 63) / 64, 512LL), U * TILE / 256));
+    const long long c = groups ? (long long)blockIdx.x * W + warp : (long long)warp * gridDim.x + blockIdx.x;
     if (c >= C) return;
     const long long u0 = kv8::first_unit(c, U, C), u1 = kv8::first_unit(c + 1, U, C);
     Cursor put;                           // the block that is copied next
@@ -451,6 +462,7 @@ __global__ void __launch_bounds__(W * 32, D == 256 || NT == 2 ? 1 : 2) kv8_decod
         put.head = (int)((u0 - put.ub) / put.nt);
         set_segment(a, put, u0, u1);
     }
+    const long long pair0 = put.ub + (long long)put.head * put.nt, pair1 = pair0 + put.nt;
     Cursor get = put;                     // the block that is worked on next
     bool more = true;                     // put is at a block
     // bit s: stage s holds a block (a page that is not there leaves its tokens out)
@@ -476,6 +488,8 @@ __global__ void __launch_bounds__(W * 32, D == 256 || NT == 2 ? 1 : 2) kv8_decod
 #pragma unroll
     for (int s = 0; s < R::S - 1; ++s) issue(s);
     int stage = 0;
+    // the CTA's ranges are inside one pair (the same for all its warps)
+    const bool joined = groups && kv8::first_unit(c - warp, U, C) >= pair0 && kv8::first_unit(c - warp + W, U, C) <= pair1;
 
     while (true) {
         const size_t row0 = ((size_t)get.b * a.Hkv + get.head) * (size_t)a.G;
@@ -500,7 +514,18 @@ __global__ void __launch_bounds__(W * 32, D == 256 || NT == 2 ? 1 : 2) kv8_decod
 
         // the segment's end: l over the lanes, then out, or this part to the workspace
         const bool whole = get.first == 0 && get.last == get.nt;
-        const size_t slot = 2 * (size_t)c + (get.ub + (long long)get.head * get.nt + get.first == u0 ? 0 : 1);
+        const long long us = get.ub + (long long)get.head * get.nt;
+        const size_t slot = 2 * (size_t)c + (us + get.first == u0 ? 0 : 1);
+        float *part = a.ws_o + slot * a.G * D, *part_ml = a.ws_ml + slot * a.G * 2;
+        int ld = D;
+        if (joined) {
+            // to shared memory instead, where every warp is done with its ring
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            __syncthreads();
+            part = reinterpret_cast<float *>(smem) + warp * NH * LD;
+            part_ml = &sm_ml[warp][0].x;
+            ld = LD;
+        }
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -523,23 +548,45 @@ __global__ void __launch_bounds__(W * 32, D == 256 || NT == 2 ? 1 : 2) kv8_decod
                             }
                             *reinterpret_cast<uint4 *>(a.out + (row0 + h) * D + d0) = make_uint4(w[0], w[1], w[2], w[3]);
                         } else {
-                            float *to = a.ws_o + (slot * a.G + h) * D + d0;
+                            float *to = part + h * ld + d0;
                             *reinterpret_cast<float4 *>(to) = make_float4(o[n][j][e], o[n][j][e + 2], o[n][j + 1][e], o[n][j + 1][e + 2]);
                             *reinterpret_cast<float4 *>(to + 4) = make_float4(o[n][j + 2][e], o[n][j + 2][e + 2], o[n][j + 3][e], o[n][j + 3][e + 2]);
                         }
                     }
-                    if (!whole && g == 0) {
-                        a.ws_ml[(slot * a.G + h) * 2] = m[n][e];
-                        a.ws_ml[(slot * a.G + h) * 2 + 1] = l[n][e];
-                    }
+                    if (!whole && g == 0) *reinterpret_cast<float2 *>(part_ml + 2 * h) = make_float2(m[n][e], l[n][e]);
                 }
             }
         if (get.first == 0 && lane == 0) {
-            const long long us = get.ub + (long long)get.head * get.nt;
-            const int n = whole ? 1 : kv8::worker_of_unit(us + get.nt - 1, U, C) - (int)c + 1;
-            a.ws_parts[(size_t)get.b * a.Hkv + get.head] = make_int2((int)slot, n);
+            const kv8::Parts p = whole ? kv8::Parts{1, 0, 0} : kv8::pair_parts((int)c, us > u0, us + get.nt, U, C, groups ? W : 0);
+            a.ws_parts[(size_t)get.b * a.Hkv + get.head] = make_int2((int)slot, kv8::pack_parts(p));
         }
         if (!next_segment(a, get, u1)) break;
+    }
+    if (joined) {
+        // one part in the first warp's slot: M = max m_w, sum O_w 2^(m_w - M), in order
+        __syncthreads();
+        const size_t at = 2 * (size_t)(c - warp) * a.G;
+#pragma unroll 1
+        for (int i = threadIdx.x * 4; i < a.G * D; i += W * 128) {
+            const int h = i / D, d = i % D;
+            float M = -INFINITY, L = 0.0f;
+#pragma unroll
+            for (int w = 0; w < W; ++w) M = fmaxf(M, sm_ml[w][h].x);
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                const float2 ml = sm_ml[w][h];
+                const float f = ml.x == -INFINITY ? 0.0f : ex2(ml.x - M);
+                const float4 x = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(smem) + (w * NH + h) * LD + d);
+                L = fmaf(ml.y, f, L);
+                s.x = fmaf(x.x, f, s.x);
+                s.y = fmaf(x.y, f, s.y);
+                s.z = fmaf(x.z, f, s.z);
+                s.w = fmaf(x.w, f, s.w);
+            }
+            *reinterpret_cast<float4 *>(a.ws_o + at * D + i) = s;
+            if (d == 0) *reinterpret_cast<float2 *>(a.ws_ml + (at + h) * 2) = make_float2(M, L);
+        }
     }
     if (bad && lane == 0) atomicExch(a.status, (int)W4A8_ERR_PAGE);
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -711,8 +758,8 @@ __global__ void __launch_bounds__(W * 32, 1) kv8_decode_pair_kernel(const Decode
 //   M = max m_s,  out = sum_s o_s 2^(m_s - M) / sum_s l_s 2^(m_s - M),
 // the parts spread over groups of threads that hold the share of d, and folded
 // in a fixed order.  Few pairs have many parts each (one sequence of 131072
-// tokens: 1216), and one SM reads them at its own rate: the shares of d spread
-// them over four times as many.
+// tokens on 2 KV heads: 152), and one SM reads them at its own rate: the shares of
+// d spread them over four times as many.
 constexpr int NC = 1024;             // threads at most
 
 __global__ void __launch_bounds__(NC) kv8_combine_kernel(const DecodeArgs a, int D) {
@@ -731,10 +778,12 @@ __global__ void __launch_bounds__(NC) kv8_combine_kernel(const DecodeArgs a, int
         for (int i = threadIdx.x; i < Dz; i += nt) a.out[out_at + i] = 0;
         return;
     }
-    const int n = parts.y;
-    if (n <= 1) return;
+    const kv8::Parts pp = kv8::unpack_parts(parts.y);
+    const int n = pp.head + pp.ctas + pp.tail;
+    if (pp.head == 1 && n == 1) return;
+    const int first = parts.x >> 1;
     // the first part is in the slot that its worker named, the others in their workers' first
-    auto slot = [&](int p) { return p == 0 ? parts.x : (parts.x & ~1) + 2 * p; };
+    auto slot = [&](int p) { return p == 0 ? parts.x : 2 * kv8::part_worker(first, pp, W, p); };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float M = -INFINITY, m0 = 0.0f, l0 = 0.0f;               // (the first pair is kept: one round trip for up to nt parts)
     for (int p = threadIdx.x; p < n; p += nt) {
@@ -814,12 +863,13 @@ int split_workers(int B, int Hq, int Hkv, int D, int T, int maxp) {
 
 // CTAs of a pair's cluster for the pair kernel, 0 where the split kernel runs.
 // The pair kernel saves the second launch and the parts' way through memory,
-// but a sequence is bound to its cluster.  Measured (split / pair, us, pairs of
-// D = 128): tables of 512 tokens 12.3 / 9.6 for one pair, 22.6 / 8.9 for 152,
-// 34.9 / 22.9 for 600; of 4096 tokens 12.5 / 11.7, 42.6 / 31.7, 123.8 / 100.4
-// where all are full and 13.4 / 12.0, 34.1 / 29.7, 76.4 / 70.3 where their
-// lengths are spread; of 8192 tokens 14.4 / 15.0 for one pair and, spread, 45.8
-// / 52.6 for 152.  So the split kernel takes over above 4096.
+// but a sequence is bound to its cluster.  Measured (split / pair, us a call,
+// pairs of D = 128): tables of 512 tokens 9.2 / 6.1 for one pair, 13.2 / 7.7 for
+// 152, 30.1 / 19.5 for 600; of 4096 tokens 10.2 / 8.4, 35.9 / 28.0, 121.4 / 95.8
+// where all are full and 10.6 / 7.6, 24.1 / 34.7, 73.3 / 63.7 where their lengths
+// are spread.  The pair kernel's lead shrinks with the length (one pair: 3.1 us at
+// 512, 1.8 at 4096) and is lost at 152 spread pairs, so the split kernel takes
+// over above 4096.
 int pair_ctas(int B, int Hkv, int T, int maxp) {
     const long long cap = (long long)maxp * T, pairs = (long long)B * Hkv;
     if (cap > PAIR_TOKENS) return 0;
@@ -914,10 +964,12 @@ w4a8_status launch_kv8_decode(const uint16_t *q, const Kv8Cache &c, const int32_
     if (c.D == 128) st = G <= 8 ? launch_decode<128, 1>(a, C, stream) : launch_decode<128, 2>(a, C, stream);
     if (c.D == 256) st = G <= 8 ? launch_decode<256, 1>(a, C, stream) : launch_decode<256, 2>(a, C, stream);
     if (st != W4A8_OK) return st;
-    // threads: a group (a share of d) for about 4 parts (a part for each worker
-    // of a pair, up to one for each 64 tokens); four shares of d where a pair has
-    // more parts than the threads of one CTA take at once
-    long long parts = workers / ((long long)B * c.Hkv) + 1;
+    // threads: a group (a share of d) for about 4 parts (one for each worker of a
+    // pair, up to one for each unit, or for each CTA of its workers where the split
+    // joins them); four shares of d where a pair has more parts than the threads
+    // of one CTA take at once
+    const long long pairs = (long long)B * c.Hkv;
+    long long parts = workers >= 2 * W * pairs ? workers / (W * pairs) + 2 * W : workers / pairs + 1;
     const long long tiles = ((long long)maxp * c.T + TILE - 1) / TILE;
     if (parts > tiles) parts = tiles;
     const int z = parts > NC / (c.D / 4) * 4 ? 4 : 1, per = c.D / 4 / z;

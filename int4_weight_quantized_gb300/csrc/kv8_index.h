@@ -59,4 +59,27 @@ KV8_FN int touched_blocks(int start, int n) { return (start % kBlockTokens + n -
 KV8_FN long long first_unit(long long c, long long U, long long C) { return c * U / C; }
 KV8_FN int worker_of_unit(long long u, long long U, long long C) { return (int)(((u + 1) * C - 1) / U); }
 
+// The parts of a pair whose units end before `end`, and whose first part is that
+// of worker `first` (cut: its range begins before the pair), in order: `head`
+// workers', then one each of `ctas` groups of W workers (c / W the group), then
+// `tail` workers'.  A group has one part where all its ranges are inside the
+// pair; with W = 0 none has.
+struct Parts { int head, ctas, tail; };
+KV8_FN Parts pair_parts(int first, bool cut, long long end, long long U, long long C, int W) {
+    const int last = worker_of_unit(end - 1, U, C);
+    if (W > 0) {
+        const int lo = first + cut, hi = last + 1 - (first_unit(last + 1, U, C) > end);
+        const int a = (lo + W - 1) / W, b = hi / W;
+        if (a < b) return {a * W - first, b - a, last + 1 - b * W};
+    }
+    return {last + 1 - first, 0, 0};
+}
+KV8_FN int pack_parts(Parts p) { return p.head | p.tail << 12 | p.ctas << 16; }
+KV8_FN Parts unpack_parts(int v) { return {v & 0xfff, v >> 16, (v >> 12) & 0xf}; }
+// The worker that has part i (a group's first worker its part).
+KV8_FN int part_worker(int first, Parts p, int W, int i) {
+    const int k = i - p.head, groups = k < 0 ? 0 : k < p.ctas ? k : p.ctas;      // groups before part i
+    return first + i + (W - 1) * groups;
+}
+
 }  // namespace kv8

@@ -11,4 +11,10 @@ int item_count(int rows, int unit, int slack, int B) { return kv8::item_count(ro
 int touched_blocks(int start, int n) { return kv8::touched_blocks(start, n); }
 long long first_unit(long long c, long long U, long long C) { return kv8::first_unit(c, U, C); }
 int worker_of_unit(long long u, long long U, long long C) { return kv8::worker_of_unit(u, U, C); }
+// out: head, ctas, tail, after a way through the packed form
+void pair_parts(int first, int cut, long long end, long long U, long long C, int W, int *out) {
+    const kv8::Parts p = kv8::unpack_parts(kv8::pack_parts(kv8::pair_parts(first, cut != 0, end, U, C, W)));
+    out[0] = p.head, out[1] = p.ctas, out[2] = p.tail;
+}
+int part_worker(int first, int head, int ctas, int tail, int W, int i) { return kv8::part_worker(first, {head, ctas, tail}, W, i); }
 }

@@ -247,6 +247,29 @@ def test_decode_long_and_short(w4, D, T):
     _verify_decode(out, q, cache, table, lens, T)
 
 
+@pytest.mark.parametrize("D,Hq,H,T,lens", [
+    (64, 16, 1, 16, [30000]), (64, 24, 3, 128, [70001, 5000]), (128, 32, 2, 32, [20000, 0, 9000]), (128, 10, 2, 64, [8192] * 4),
+    (256, 16, 1, 64, [4097, 33333]), (256, 5, 1, 128, [100000])])
+def test_decode_parts_joined_on_chip(w4, D, Hq, H, T, lens):
+    # few long pairs: CTAs inside one pair join their warps' parts, those over a
+    # pair's end do not; one stretch of the last sequence is on no page
+    P = sum(-(-n // T) for n in lens) + 1
+    cache = _random_cache(w4, P, H, T, D, seed=T + D)
+    table = _table(lens, T, P, seed=2)
+    n = lens[-1] // T
+    table[-1, n // 4:n // 2] = -1
+    q = torch.randn((len(lens), Hq, D), generator=torch.Generator().manual_seed(D)).half()
+    out = w4.decode_attention_kv8(q.cuda(), cache, _i32(table), _i32(lens))
+    assert w4.get_device_status() == ERR_PAGE
+    keep = [x for i, x in enumerate(table[-1]) if not n // 4 <= i < n // 2]
+    held = np.full_like(table, -1)
+    held[:-1] = table[:-1]
+    held[-1, :len(keep)] = keep
+    _verify_decode(out, q, cache, held, lens[:-1] + [lens[-1] - (n // 2 - n // 4) * T], T)
+    again = w4.decode_attention_kv8(q.cuda(), cache, _i32(table), _i32(lens))
+    assert torch.equal(out, again) and w4.get_device_status() == ERR_PAGE
+
+
 @pytest.mark.parametrize("extra", [0, 300])
 def test_decode_many_sequences(w4, extra):
     rs = np.random.RandomState(5)

@@ -83,3 +83,34 @@ def test_work_ranges_cover_all_units(X):
         for u in {0, U - 1, *(rng.randrange(U) for _ in range(50)), *(x for x in cuts[:-1]), *(x - 1 for x in cuts[1:])}:
             c = X.worker_of_unit(u, U, C)
             assert cuts[c] <= u < cuts[c + 1]
+
+
+@pytest.mark.parametrize("W", [0, 8])
+def test_pair_parts_take_every_worker_once(X, W):
+    rng = random.Random(17 + W)
+    out, seen = (ctypes.c_int * 3)(), set()
+    for _ in range(400):
+        C = 8 * rng.choice([1, 2, 3, 19, 152, 304])
+        sizes = [rng.choice([1, 7, 8, 9, rng.randrange(1, 3000), rng.randrange(1, 10 ** 6)]) for _ in range(rng.randint(1, 6))]
+        sizes[0] += max(0, C - sum(sizes))
+        U, us = sum(sizes), 0
+        cuts = [X.first_unit(c, U, C) for c in range(C + 1)]
+        for nt in sizes:
+            first, last = X.worker_of_unit(us, U, C), X.worker_of_unit(us + nt - 1, U, C)
+            X.pair_parts(first, cuts[first] < us, us + nt, U, C, W, out)
+            head, ctas, tail = out
+            got = []
+            for i in range(head + ctas + tail):
+                c = X.part_worker(first, head, ctas, tail, W, i)
+                whole = head <= i < head + ctas
+                # a group's part is its first worker's; the whole group is inside the pair
+                assert not whole or (c % W == 0 and cuts[c] >= us and cuts[c + W] <= us + nt)
+                got += range(c, c + W) if whole else [c]
+            assert got == list(range(first, last + 1))
+            # and every group that is inside the pair has one part
+            inside = [k for k in range(C // 8) if W and cuts[8 * k] >= us and cuts[8 * k + 8] <= us + nt]
+            assert len(inside) == ctas
+            seen.add((head > 0, ctas > 0, tail > 0))
+            us += nt
+    # without groups every part is a worker's of the head; with them any of the five forms that there are
+    assert len(seen) == (1 if W == 0 else 5)
