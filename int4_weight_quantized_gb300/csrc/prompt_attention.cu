@@ -52,6 +52,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "kv8.cuh"
+#include "prompt_ring.h"
 #include "sync.cuh"
 #include "tc.cuh"
 
@@ -71,7 +72,7 @@ struct Cfg {
     static constexpr int SD = D < 128 ? D : 128;             // dims per ring slot
     static constexpr int SPT = D / SD;                       // slots per K or V tile
     static constexpr int SLOT = BN * SD * 2;
-    static constexpr int NSLOT = 5;
+    static constexpr int NSLOT = prompt_ring::kSlots;
     static constexpr int QTILE = 128 * D * 2;
     static constexpr int GROUPS = NQ;                        // softmax groups of 4 warps
     static constexpr int THREADS = (4 * GROUPS + 2) * 32;
@@ -465,8 +466,8 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         const int all_see = a.causal ? min(job.nk, job.t0 + grp * a.tok + off + 1) : job.nk;
         float m = -INFINITY, l = 0.0f;
         bool ok = true;
-        // V(j)'s tile of the ring, in the order of loading
-        auto v_tile = [&](int j) { return C::K_FIRST && j + 1 < nmax ? 2 * j + 2 : 2 * j + 1; };
+        // half h of V(j): its item of the ring
+        auto v_item = [&](int j, int h) { return prompt_ring::v_tile(j, nmax, C::K_FIRST) * C::SPT + h; };
         // the first diagonal tile of the CTA's rows; they see the diagonal's keys in
         // up to 3 tiles (at most 256 tokens)
         const int diag0 = max(job.t0 + off, 0) / BN;
@@ -480,8 +481,8 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             bool w = true;
 #pragma unroll
             for (int h = 0; h < C::SPT; ++h) {
-                const int at = v_tile(j) * C::SPT + h, slot = at % C::NSLOT;
-                w = w && wait.warp(&full[slot], (uint32_t)(at / C::NSLOT) & 1u);
+                const int slot = prompt_ring::slot_of(v_item(j, h));
+                w = w && wait.warp(&full[slot], prompt_ring::parity_of(v_item(j, h)));
                 if (!w) return false;
                 const uint8_t *row = smem + C::OFF_RING + slot * C::SLOT + r * 128;
 #pragma unroll 4
@@ -507,7 +508,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             if (bad) {
 #pragma unroll
                 for (int h = 0; h < C::SPT; ++h) {
-                    const int slot = (v_tile(j) * C::SPT + h) % C::NSLOT;
+                    const int slot = prompt_ring::slot_of(v_item(j, h));
                     for (int c = 0; c < C::SD / 2; ++c) {
                         uint32_t *x = reinterpret_cast<uint32_t *>(smem + C::OFF_RING + slot * C::SLOT + (c >> 5) * (BN * 128) + r * 128) + (c & 31);
                         *x &= ~__vcmpeq2(*x & inf, inf);
@@ -522,8 +523,8 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             bool w = true;
 #pragma unroll
             for (int h = 0; h < C::SPT; ++h) {
-                const int at = v_tile(j) * C::SPT + h, slot = at % C::NSLOT;
-                w = w && wait.warp(&full[slot], (uint32_t)(at / C::NSLOT) & 1u);
+                const int slot = prompt_ring::slot_of(v_item(j, h));
+                w = w && wait.warp(&full[slot], prompt_ring::parity_of(v_item(j, h)));
                 if (!w) return false;
                 for (int x = r; x < rows * (C::SD / 8); x += 128) {
                     const int row = row0 + x / (C::SD / 8), q = x % (C::SD / 8);
@@ -539,6 +540,11 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             const uint32_t ph = (uint32_t)(C::NQ == 1 ? j / C::NS : j) & 1u;
             // (here, where no scores are held in registers)
             if (a.causal && (j + 1) * BN > all_see) {
+                if constexpr (prompt_ring::screen_after_products(C::SPT)) {
+                    // else V(j)'s barriers may still be at the items before it
+                    ok = wait.warp(&sbar[buf], ph) && (j == 0 || wait.warp(&obar[grp], (uint32_t)(j - 1) & 1u));
+                    if (!ok) break;
+                }
                 ok = screen_rows(j);
                 if (!ok) break;
             }
