@@ -142,6 +142,16 @@ def _need(t, dtype, shape, name):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _workspace(t):
+    """A workspace's pointer and bytes (NULL and 0 for None).  It has to be contiguous: an
+    expanded tensor counts more bytes than it has."""
+    if t is None:
+        return _p(None), 0
+    if not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return _p(t), t.numel()
+
+
 def packed_bytes(N, K):
     return lib().w4a8_packed_bytes(N, K)
 
@@ -213,9 +223,9 @@ def linear(x, packed, scales, out=None, path=PATH_AUTO, workspace=None):
     need = workspace_bytes(M, N, K, path)
     if need and workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-    wsb = workspace.numel() if workspace is not None else 0
+    ws, wsb = _workspace(workspace)
     _check(lib().w4a8_linear_ex(_p(x), _p(packed), _p(scales), M, N, K, _p(out), path,
-                                _p(workspace), wsb, _stream()), "w4a8_linear_ex")
+                                ws, wsb, _stream()), "w4a8_linear_ex")
     return out
 
 
@@ -240,9 +250,9 @@ def linear_gated(x, packed_gu, scales_gu, act=ACT_SILU, out=None, workspace=None
     need = gated_workspace_bytes(M, N, K)
     if need and workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-    wsb = workspace.numel() if workspace is not None else 0
+    ws, wsb = _workspace(workspace)
     _check(lib().w4a8_linear_gated(_p(x), _p(packed_gu), _p(scales_gu), M, N, K, _p(out), int(act),
-                                   _p(workspace), wsb, _stream()), "w4a8_linear_gated")
+                                   ws, wsb, _stream()), "w4a8_linear_gated")
     return out
 
 
@@ -281,8 +291,8 @@ def linear_q8(codes, sx, packed, scales, out=None, workspace=None):
     need = lib().w4a8_linear_q8_workspace_bytes(M, N, K)
     if need and workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=codes.device)
-    wsb = workspace.numel() if workspace is not None else 0
-    _check(lib().w4a8_linear_q8(_p(codes), _p(sx), _p(packed), _p(scales), M, N, K, _p(out), _p(workspace), wsb,
+    ws, wsb = _workspace(workspace)
+    _check(lib().w4a8_linear_q8(_p(codes), _p(sx), _p(packed), _p(scales), M, N, K, _p(out), ws, wsb,
                                 _stream()), "w4a8_linear_q8")
     return out
 
@@ -302,9 +312,9 @@ def decode_attention(q, k_cache, v_cache, lens, out=None, workspace=None):
     need = lib().w4a8_decode_attention_workspace_bytes(B, Hq, Hkv, D, Lmax)
     if need and workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    wsb = workspace.numel() if workspace is not None else 0
+    ws, wsb = _workspace(workspace)
     _check(lib().w4a8_decode_attention(_p(q), _p(k_cache), _p(v_cache), _p(lens), B, Hq, Hkv, D, Lmax, _p(out),
-                                       _p(workspace), wsb, _stream()), "w4a8_decode_attention")
+                                       ws, wsb, _stream()), "w4a8_decode_attention")
     return out
 
 
@@ -411,9 +421,9 @@ def debug_block_dots(x, packed, scales, path=PATH_AUTO, workspace=None):
     need = workspace_bytes(M, N, K, path)
     if need and workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-    wsb = workspace.numel() if workspace is not None else 0
+    ws, wsb = _workspace(workspace)
     _check(lib().w4a8_debug_block_dots(_p(x), _p(packed), _p(scales), M, N, K, _p(dots), _p(out), path,
-                                       _p(workspace), wsb, _stream()), "w4a8_debug_block_dots")
+                                       ws, wsb, _stream()), "w4a8_debug_block_dots")
     return dots, out
 
 

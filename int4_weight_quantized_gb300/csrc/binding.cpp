@@ -112,6 +112,13 @@ Tensor output(PyObject *o, const char *name, at::ScalarType dtype, at::IntArrayR
     return at::empty(shape, like.options().dtype(dtype));
 }
 
+// The caller's workspace has to be contiguous: an expanded tensor counts more
+// bytes than it has.  Looked at before the other arguments.
+void check_workspace(PyObject *o) {
+    if (o != Py_None && THPVariable_Check(o) && !THPVariable_Unpack(o).is_contiguous())
+        throw BadArgument{PyExc_ValueError, "workspace must be contiguous"};
+}
+
 Tensor workspace(PyObject *o, size_t need, const Tensor &like) {
     if (o != Py_None) return tensor(o, "workspace", at::kByte);
     return at::empty({(int64_t)need}, like.options().dtype(at::kByte));
@@ -202,6 +209,7 @@ PyObject *kv8_read(Args a) {
 
 // (q, cache, table, lens, scale, out, workspace)
 PyObject *decode_attention_kv8(Args a) {
+    check_workspace(a[6]);
     const w4a8_kv8 c = cache_of(a[1]);
     const Table t = table_of(a[2]);
     dims(a[0], "q", 3, at::kHalf);
@@ -245,6 +253,7 @@ PyObject *kv8_fork(Args a) {
 
 // (cache, table, lens, table_out, count, workspace)
 PyObject *kv8_compact(Args a) {
+    check_workspace(a[5]);
     const w4a8_kv8 c = cache_of(a[0]);
     const Table t = table_of(a[1]);
     const Tensor &like = THPVariable_Unpack(a[1]);
