@@ -118,7 +118,7 @@ __device__ __forceinline__ int seq_len(const DecodeArgs &a, int b) {
     const int n = a.lens[b];
     return n < 0 ? 0 : (n > most ? (int)most : n);
 }
-__device__ __forceinline__ int seq_tiles(const DecodeArgs &a, int b) { return (seq_len(a, b) + TILE - 1) / TILE; }
+__device__ __forceinline__ int seq_tiles(const DecodeArgs &a, int b) { return kv8::tile_count(seq_len(a, b), TILE); }
 
 // Sum over the CTA's threads of up to 1024; every thread gets the total and
 // the sum of the threads before it.
@@ -158,7 +158,7 @@ __device__ __forceinline__ void set_segment(const DecodeArgs &a, Cursor &c, long
     c.first = first;
     c.last = last;
     c.blk = first * (TILE / 16);
-    c.end = (min(c.len, last * TILE) + 15) >> 4;
+    c.end = kv8::blocks_before(c.len, last, TILE);
 }
 
 // On to the next pair; false at the range's end.
@@ -170,7 +170,7 @@ __device__ __forceinline__ bool next_segment(const DecodeArgs &a, Cursor &c, lon
         do {
             c.ub += (long long)c.nt * a.Hkv;
             c.len = seq_len(a, ++c.b);
-            c.nt = (c.len + TILE - 1) / TILE;
+            c.nt = kv8::tile_count(c.len, TILE);
         } while (c.nt == 0);
     }
     set_segment(a, c, u, u1);
@@ -453,11 +453,11 @@ __global__ void __launch_bounds__(W * 32, D == 256 || NT == 2 ? 1 : 2) kv8_decod
         put.b = (at - 1) * share;         // the last share that begins at or before u0
         put.ub = sm_scan[at - 1];
         put.len = seq_len(a, put.b);
-        put.nt = (put.len + TILE - 1) / TILE;
+        put.nt = kv8::tile_count(put.len, TILE);
         while (u0 >= put.ub + (long long)put.nt * a.Hkv) {
             put.ub += (long long)put.nt * a.Hkv;
             put.len = seq_len(a, ++put.b);
-            put.nt = (put.len + TILE - 1) / TILE;
+            put.nt = kv8::tile_count(put.len, TILE);
         }
         put.head = (int)((u0 - put.ub) / put.nt);
         set_segment(a, put, u0, u1);

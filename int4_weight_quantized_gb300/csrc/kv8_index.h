@@ -42,6 +42,15 @@ KV8_FN int held_entries(int len, int T, int maxp) {
     return n < maxp ? n : maxp;
 }
 
+// Tiles of `tile` tokens that len tokens take, and the end in blocks of a run of
+// tiles that ends before tile `last`, cut at the sequence's end: for every length
+// from 0 to 2^31 - 1 (len + tile - 1 and last * tile may pass it).
+KV8_FN int tile_count(int len, int tile) { return (int)(((unsigned)len + (unsigned)tile - 1u) / (unsigned)tile); }
+KV8_FN int blocks_before(int len, int last, int tile) {
+    const long long end = (long long)last * tile;
+    return tile_count(end < len ? (int)end : len, kBlockTokens);
+}
+
 // Packed sequences: sequence b has rows cu[b] .. cu[b+1] - 1.  Work items of
 // `unit` rows are numbered without a pass over all lengths: sequence b's
 // items begin at cu[b] / unit + slack * b.  That leaves it at least

@@ -6,6 +6,8 @@ size_t code_offset(int page, int Hkv, int head, int T, int tok, int D) { return 
 size_t scale_offset(int page, int Hkv, int head, int T, int tok) { return kv8::scale_offset(page, Hkv, head, T, tok); }
 int page_of_row(const int32_t *row, int maxp, int page, int P) { return kv8::page_of_row(row, maxp, page, P); }
 int held_entries(int len, int T, int maxp) { return kv8::held_entries(len, T, maxp); }
+int tile_count(int len, int tile) { return kv8::tile_count(len, tile); }
+int blocks_before(int len, int last, int tile) { return kv8::blocks_before(len, last, tile); }
 int item_base(int cu_b, int unit, int slack, int b) { return kv8::item_base(cu_b, unit, slack, b); }
 int item_count(int rows, int unit, int slack, int B) { return kv8::item_count(rows, unit, slack, B); }
 int touched_blocks(int start, int n) { return kv8::touched_blocks(start, n); }
