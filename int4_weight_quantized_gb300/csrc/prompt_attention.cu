@@ -464,7 +464,12 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         const int steps = steps_of[grp];
         // keys that every row of the tile sees: below it no mask is needed
         const int all_see = a.causal ? min(job.nk, job.t0 + grp * a.tok + off + 1) : job.nk;
-        float m = -INFINITY, l = 0.0f;
+        // A row's maximum moves by its own scores alone, so nothing that it does not see
+        // (the other rows of its warp: later tokens, the next sequence's, rows that a
+        // group leaves over) changes the rounding of its weights.  Rows that are no
+        // output never move: below m = inf every weight is 0.
+        const bool mine = r < a.tok * a.G && tok_i < job.nq;
+        float m = mine ? -INFINITY : INFINITY, l = 0.0f;
         bool ok = true;
         // half h of V(j): its item of the ring
         auto v_item = [&](int j, int h) { return prompt_ring::v_tile(j, nmax, C::K_FIRST) * C::SPT + h; };
@@ -572,10 +577,10 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             mx[0] = max3(mx[0], s[BN - 4], s[BN - 3]);
             mx[1] = max3(mx[1], s[BN - 2], s[BN - 1]);
             const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * a.scale_log2;
-            if (__any_sync(0xffffffffu, top > m + 8.0f)) {
-                const float mn = fmaxf(m, top);
-                const float f = m == -INFINITY ? 0.0f : ex2(m - mn);
-                m = mn;
+            const bool up = top > m + 8.0f;
+            if (__any_sync(0xffffffffu, up)) {
+                const float f = up ? ex2(m - top) : 1.0f;
+                m = up ? top : m;
                 l *= f;
                 if (j > 0) {
                     // O is at rest once the last step's product is in (the one before it
@@ -643,7 +648,6 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
         // before it)
         if (steps > 0) ok = ok && wait.warp(&fbar[grp], 0);
         tc_fence_after();
-        const bool mine = r < a.tok * a.G && tok_i < job.nq;
         uint16_t *dst = a.out + ((size_t)(job.q0 + tok_i) * a.Hq + (size_t)head * a.G + r % a.G) * D;
         const float inv = l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l);
         // Out through shared memory, in the place of this tile's Q (a tile without
