@@ -313,7 +313,8 @@ __device__ __forceinline__ void add_block(uint32_t kb, float ks, float vs, int l
             y[n][1] = in0 ? fmaf(s[n][1], ks, lw) : -INFINITY;
             y[n][2] = in1 ? fmaf(s[n][2], ks, lw) : -INFINITY;
             y[n][3] = in1 ? fmaf(s[n][3], ks, lw) : -INFINITY;
-            move = move || fmaxf(y[n][0], y[n][2]) > m[n][0] + 8.0f || fmaxf(y[n][1], y[n][3]) > m[n][1] + 8.0f;
+            // (the differences, which are exact: m + 8 would round where scores pass 2^26)
+            move = move || fmaxf(y[n][0], y[n][2]) - m[n][0] > 8.0f || fmaxf(y[n][1], y[n][3]) - m[n][1] > 8.0f;
         }
         if (__any_sync(0xffffffffu, move)) {
 #pragma unroll

@@ -577,7 +577,8 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             mx[0] = max3(mx[0], s[BN - 4], s[BN - 3]);
             mx[1] = max3(mx[1], s[BN - 2], s[BN - 1]);
             const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * a.scale_log2;
-            const bool up = top > m + 8.0f;
+            // (the difference, which is exact: m + 8 would round where scores pass 2^26)
+            const bool up = top - m > 8.0f;
             if (__any_sync(0xffffffffu, up)) {
                 const float f = up ? ex2(m - top) : 1.0f;
                 m = up ? top : m;

@@ -1,5 +1,4 @@
-"""Prompt attention on the GPU: what a row does not see changes nothing of it, bit
-for bit, and weights far below the largest still count."""
+"""Prompt attention on the GPU: what a row does not see changes nothing of it, bit for bit."""
 import numpy as np
 import pytest
 import torch
