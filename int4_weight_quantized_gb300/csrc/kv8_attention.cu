@@ -35,10 +35,12 @@
 //
 // Softmax.  x = (scale log2 e s_k) S in fp32.  V's scale goes into the weight:
 // p' = s_v 2^(x - m) multiplies the codes, the running maximum m being of
-// x + log2 s_v, and l sums 2^(x - m) = p' / s_v in fp32.  p' is rounded to
-// fp16 for the product (2^-11 relative, unbiased); m only moves when a new
-// value exceeds it by more than 8, so p' stays below 2^9 and the accumulators
-// are rarely rescaled.
+// x + log2 s_v, less 7, and l sums 2^(x - m) = p' / s_v in fp32.  m only moves when
+// a new value exceeds it by more than 15, so p' stays below 2^15 and the
+// accumulators are rarely rescaled.  p' is rounded to fp16 for the product: to
+// 2^-11 of itself down to 2^-21 of a worker's largest one (2^7 or more), to 2^-32
+// of that below, where 131072 tokens lose 2^-15 at most (with p' from 1 on the
+// small ones beside one large token were lost below 2^-25).
 #include <math.h>
 
 #include "common.cuh"
@@ -56,6 +58,8 @@ constexpr int TILE = 32;             // tokens per unit of the split
 constexpr int MAXC = 152 * 2;        // CTAs at most
 constexpr int MAXW = MAXC * W;       // workers (warps) at most
 constexpr int PAIR_TOKENS = 4096;    // tokens that a table may hold for the pair kernel
+constexpr float kLift = 7.0f;        // the running maximum is kept this much below the real one: p' = 2^7 there
+constexpr float kMargin = kLift + 8.0f;  // and moves when a value is above it by more
 constexpr float kTiny = 8.673617e-19f;   // 2^-60: stands for a zero scale in the weights (the smallest
                                          // real one, from the smallest fp16 value, is 2^-31)
 
@@ -313,8 +317,8 @@ __device__ __forceinline__ void add_block(uint32_t kb, float ks, float vs, int l
             y[n][1] = in0 ? fmaf(s[n][1], ks, lw) : -INFINITY;
             y[n][2] = in1 ? fmaf(s[n][2], ks, lw) : -INFINITY;
             y[n][3] = in1 ? fmaf(s[n][3], ks, lw) : -INFINITY;
-            // (the differences, which are exact: m + 8 would round where scores pass 2^26)
-            move = move || fmaxf(y[n][0], y[n][2]) - m[n][0] > 8.0f || fmaxf(y[n][1], y[n][3]) - m[n][1] > 8.0f;
+            // (the differences, which are exact: m + kMargin would round where scores pass 2^26)
+            move = move || fmaxf(y[n][0], y[n][2]) - m[n][0] > kMargin || fmaxf(y[n][1], y[n][3]) - m[n][1] > kMargin;
         }
         if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
@@ -324,7 +328,7 @@ __device__ __forceinline__ void add_block(uint32_t kb, float ks, float vs, int l
                     float v = fmaxf(y[n][e], y[n][e + 2]);
 #pragma unroll
                     for (int d = 4; d < 32; d <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
-                    const float mn = fmaxf(m[n][e], v);
+                    const float mn = fmaxf(m[n][e], v - kLift);
                     const float f = m[n][e] == -INFINITY ? 0.0f : ex2(m[n][e] - mn);
                     m[n][e] = mn;
                     l[n][e] *= f;

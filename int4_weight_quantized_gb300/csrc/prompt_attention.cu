@@ -33,10 +33,13 @@
 // (8 warps per tile, two threads to a row, were slower: 132 us and, at D = 128,
 // 817: what issues the products shares a quarter of the SM with them.)
 // O stays in tensor memory for the whole pass; it is rescaled
-// only when a row's maximum has grown by more than 2^8 since the one in use
-// (p then stays below 2^9, well inside fp16; the final division by the sum of
-// the same p makes the choice of m exact), which after the first tiles is
-// rare.
+// only when a row's maximum has grown by more than 2^8 since the one in use,
+// which after the first tiles is rare.  m is 7 below that maximum, so that p at
+// the maximum lies between 2^7 and 2^15 and fp16's lower range is left for small
+// weights: they are rounded to 2^-11 of themselves down to 2^-21 of the largest
+// one and to 2^-32 of it below, so that 16384 of them lose 2^-18 at most (with p
+// up to 1, 2^-14 and 2^-25: 16384 keys of weight 2^-20 lost 3 % of theirs).  The
+// sum l is of the p before they are rounded; it and O carry the same factor.
 //
 // Masked places may hold anything.  Scores are masked by selection, so K never
 // reaches a row that does not see it; with V, 0 * inf would not be 0:
@@ -61,6 +64,8 @@ namespace {
 using namespace w4a8;
 
 constexpr int BN = 128;              // keys per step
+constexpr float kLift = 7.0f;        // m is this much below the maximum when it moves: p = 2^7 there
+constexpr float kMargin = kLift + 8.0f;   // and moves when a score is above it by more: p < 2^15 (1 + 2^-20)
 constexpr long long kDrain = 1LL << 31;   // cycles that a CTA which gives up waits for what it has under way
 
 template <int D>
@@ -577,11 +582,12 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_c
             mx[0] = max3(mx[0], s[BN - 4], s[BN - 3]);
             mx[1] = max3(mx[1], s[BN - 2], s[BN - 1]);
             const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * a.scale_log2;
-            // (the difference, which is exact: m + 8 would round where scores pass 2^26)
-            const bool up = top - m > 8.0f;
+            // (the difference, which is exact: m + kMargin would round where scores pass 2^26)
+            const bool up = top - m > kMargin;
             if (__any_sync(0xffffffffu, up)) {
-                const float f = up ? ex2(m - top) : 1.0f;
-                m = up ? top : m;
+                const float next = up ? top - kLift : m;
+                const float f = up ? ex2(m - next) : 1.0f;
+                m = next;
                 l *= f;
                 if (j > 0) {
                     // O is at rest once the last step's product is in (the one before it
