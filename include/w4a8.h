@@ -255,8 +255,10 @@ w4a8_status w4a8_decode_attention(const uint16_t *q, const uint16_t *k_cache, co
  * to no sequence leave out as it was.  Neighbours in the packing never reach
  * a sequence's results, whatever they hold.
  * Requires D in {64, 128, 256}, Hq % Hkv == 0, Hq/Hkv <= 128, strides that are
- * multiples of 8 and cover a token, scale finite and > 0; Tq and Tk may be 0
- * (nothing runs when Tq is).  Needs no workspace. */
+ * multiples of 8 and cover a token, scale > 0 and scale log2(e) finite in fp32;
+ * Tq and Tk may be 0 (nothing runs when Tq is).  Needs no workspace.  Scores
+ * scale q.k below 2^27 in size give finite results (fp32 holds larger ones only to
+ * 16 and more, and a weight may overflow). */
 w4a8_status w4a8_prompt_attention(const uint16_t *q, const uint16_t *k, const uint16_t *v,
                                   long long ld_q, long long ld_k, long long ld_v,
                                   const int32_t *cu_q, const int32_t *cu_k, int B, int Tq, int Tk,
@@ -308,11 +310,12 @@ w4a8_status w4a8_kv8_read(const w4a8_kv8 *cache, const int32_t *table, const int
  *   h / (Hq/heads), fp32 scores, sums and accumulators, the weights rounded to
  *   fp16 before the product with v's codes.  q, out [B][Hq][dim] fp16.
  * Tokens on no page are left out.  Requires Hq % heads == 0, Hq/heads <= 16,
- * B <= 65535, max_pages * page_tokens < 2^31, scale finite and > 0, and a
- * workspace of w4a8_decode_attention_kv8_workspace_bytes (0 for an invalid
- * shape, and for tables of up to 4096 tokens, which one launch with a cluster
- * per sequence and KV head takes; above, the sequences are cut over the whole
- * GPU, and the workspace does not grow with their length). */
+ * B <= 65535, max_pages * page_tokens < 2^31, scale > 0 and scale log2(e)
+ * finite in fp32, and a workspace of
+ * w4a8_decode_attention_kv8_workspace_bytes (0 for an invalid shape, and for
+ * tables of up to 4096 tokens, which one launch with a cluster per sequence and
+ * KV head takes; above, the sequences are cut over the whole GPU, and the
+ * workspace does not grow with their length). */
 size_t w4a8_decode_attention_kv8_workspace_bytes(int B, int Hq, int Hkv, int D, int page_tokens, int max_pages);
 w4a8_status w4a8_decode_attention_kv8(const uint16_t *q, const w4a8_kv8 *cache, const int32_t *table,
                                       const int32_t *lens, int B, int Hq, int max_pages, float scale, uint16_t *out,

@@ -8,6 +8,8 @@
 // моделей"; "谷歌突然开源！端侧 AI 的 GPU 底座，要变了", m.x-techcon.com,
 // section "对大模型，重点已经从“算得快”变成“数据少搬”").  Here the phase is
 // read off M: a few tokens per call is decode, a long sequence is prefill.
+#include <float.h>
+
 #include <atomic>
 #include <mutex>
 
@@ -59,7 +61,8 @@ bool head_dim_ok(int D) { return D == 64 || D == 128 || D == 256; }
 
 bool page_tokens_ok(int T) { return T == 16 || T == 32 || T == 64 || T == 128; }
 
-bool scale_ok(float s) { return s > 0.0f && s <= 3.0e38f; }
+// A softmax's scale: the kernels work with scale log2(e), which has to be finite too.
+bool scale_ok(float s) { return s > 0.0f && s * 1.4426950408889634f <= FLT_MAX; }
 
 // Rows of heads x D with `ld` elements between tokens: TMA and the 16-byte
 // loads want multiples of 16 bytes, and a tensor map's strides end at 2^40.
