@@ -105,7 +105,10 @@ def _ext():
         lib()
         spec = importlib.util.spec_from_file_location("_w4a8", os.path.join(_HERE, "_build", "_w4a8.so"))
         if spec is None or not os.path.exists(spec.origin):
-            raise RuntimeError("_build/_w4a8.so is missing (run int4_weight_quantized_gb300.build.build())")
+            from .build import binding_error
+            why = binding_error()
+            raise RuntimeError("_build/_w4a8.so is missing (run int4_weight_quantized_gb300.build.build(force=True))"
+                               + (": it was not built: " + why if why else ""))
         _native = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(_native)
     return _native
