@@ -114,8 +114,17 @@ def test_one_long_sequence_equals_its_parts(w4, D, T, n, pieces):
     assert bool(((one - merged).abs() <= tol).all()), float(((one - merged).abs() / tol).max())
 
 
+@pytest.fixture
+def one_thread():
+    """Tests that fork may follow: no threads of torch are left behind."""
+    n = torch.get_num_threads()
+    torch.set_num_threads(1)
+    yield
+    torch.set_num_threads(n)
+
+
 @pytest.mark.parametrize("D,Hq,H,T,lens", LONG)
-def test_the_bound_shows_a_lost_tile(D, Hq, H, T, lens):
+def test_the_bound_shows_a_lost_tile(one_thread, D, Hq, H, T, lens):
     # on the CPU: leaving any 32 consecutive tokens out, or counting them twice, passes the bound several times
     k, v = _tokens(lens, H, D, seed=D + T)
     at = 0
