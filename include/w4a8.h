@@ -248,12 +248,14 @@ w4a8_status w4a8_decode_attention(const uint16_t *q, const uint16_t *k_cache, co
  *   out      [Tq][Hq][D] fp16, dense
  *   out[i][h] = sum_j softmax_j(scale q_i.k_j) v_j over the sequence's keys,
  *            KV head h / (Hq/Hkv), fp32 scores, sums and accumulators, the
- *            weights rounded to fp16 before the product with v.
+ *            weights rounded to fp16 before the product with v (to 2^-11 of
+ *            themselves, or to 2^-32 of the row's largest where that is more).
  * A sequence's queries are its last tokens: with nq queries and nk keys, query
  * i is at place i + nk - nq, and where `causal` is not 0 it sees the keys up
  * to that place.  A query that sees no key gets zeros; rows of q that belong
  * to no sequence leave out as it was.  Neighbours in the packing never reach
- * a sequence's results, whatever they hold.
+ * a sequence's results, whatever they hold: a row's bits follow from its own
+ * query and the keys and values that it sees.
  * Requires D in {64, 128, 256}, Hq % Hkv == 0, Hq/Hkv <= 128, strides that are
  * multiples of 8 and cover a token, scale > 0 and scale log2(e) finite in fp32;
  * Tq and Tk may be 0 (nothing runs when Tq is).  Needs no workspace.  Scores
@@ -307,15 +309,17 @@ w4a8_status w4a8_kv8_read(const w4a8_kv8 *cache, const int32_t *table, const int
 /* Decode attention over the 8-bit cache, one new token per sequence:
  *   out[b][h] = sum_t softmax_t(scale q[b][h].k_t) v_t, t < lens[b] (clamped
  *   to [0, max_pages page_tokens]; zeros for a length of 0), KV head
- *   h / (Hq/heads), fp32 scores, sums and accumulators, the weights rounded to
- *   fp16 before the product with v's codes.  q, out [B][Hq][dim] fp16.
+ *   h / (Hq/heads), fp32 scores, sums and accumulators, the weights times v's
+ *   scale rounded to fp16 before the product with v's codes (as above).  q, out
+ *   [B][Hq][dim] fp16.
  * Tokens on no page are left out.  Requires Hq % heads == 0, Hq/heads <= 16,
  * B <= 65535, max_pages * page_tokens < 2^31, scale > 0 and scale log2(e)
  * finite in fp32, and a workspace of
  * w4a8_decode_attention_kv8_workspace_bytes (0 for an invalid shape, and for
  * tables of up to 4096 tokens, which one launch with a cluster per sequence and
  * KV head takes; above, the sequences are cut over the whole GPU, and the
- * workspace does not grow with their length). */
+ * workspace does not grow with their length).  A workspace may be kept for calls
+ * of other shapes on the same stream, whatever it holds. */
 size_t w4a8_decode_attention_kv8_workspace_bytes(int B, int Hq, int Hkv, int D, int page_tokens, int max_pages);
 w4a8_status w4a8_decode_attention_kv8(const uint16_t *q, const w4a8_kv8 *cache, const int32_t *table,
                                       const int32_t *lens, int B, int Hq, int max_pages, float scale, uint16_t *out,

@@ -343,7 +343,8 @@ def kv8_cache(pages, heads, page_tokens, dim, device="cuda"):
 def prompt_attention(q, k, v, cu_q, cu_k=None, causal=True, scale=None, out=None):
     """Attention of packed prompts: q fp16 [Tq][Hq][D], k and v fp16 [Tk][Hkv][D] (any stride
     between tokens: parts of a fused projection's output will do), cu_q and cu_k int32 [B+1]
-    (device; cu_k = cu_q when not given), scale 1/sqrt(D) when not given -> fp16 [Tq][Hq][D]
+    (device; cu_k = cu_q when not given), scale 1/sqrt(D) when not given -> fp16 [Tq][Hq][D].
+    Rows of q that belong to no sequence are not written: of a new `out` they hold anything
     (w4a8_prompt_attention)."""
     return _result(_ext().prompt_attention(q, k, v, cu_q, cu_k, causal, scale, out), "w4a8_prompt_attention")
 
@@ -357,7 +358,8 @@ def kv8_append(cache, k, v, table, start, cu):
 
 def kv8_read(cache, table, cu, total, k_out=None, v_out=None):
     """Read tokens back: sequence b's first cu[b+1]-cu[b] tokens into rows from cu[b] of two
-    fp16 [total][heads][dim] tensors, which are returned (w4a8_kv8_read)."""
+    fp16 [total][heads][dim] tensors, which are returned; rows of no sequence are not written
+    (w4a8_kv8_read)."""
     return _result(_ext().kv8_read(cache, table, cu, total, k_out, v_out), "w4a8_kv8_read")
 
 

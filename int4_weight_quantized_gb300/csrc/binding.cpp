@@ -4,9 +4,9 @@
 // Marshalling only, like the ctypes binding of the other operators: checks of
 // the tensors, output allocation from torch's caching allocator, one call of
 // the C ABI on the current torch stream.  A decode step calls these once or
-// twice per layer, and through ctypes the checks and conversions of one call
-// took longer than its kernels (21 us against 13 for one sequence of 640
-// tokens); here they take under 2.
+// twice per layer, and through ctypes one call took longer than its kernel (21 us
+// on the host, 5 of them in the C ABI, against 7 for one sequence of 640 tokens);
+// here it takes 5, the C ABI's included (7 with the split kernel's two launches).
 //
 // Each function returns its outputs, or the library's status as an int where
 // that is not W4A8_OK (the package turns it into a W4A8Error).

@@ -17,14 +17,19 @@
 //
 // Tiles.  A warp takes 16 tokens (one scale block) at a time.  Its own ring of
 // asynchronous copies in shared memory keeps the next blocks' K, V and scales
-// in flight while it works on one: 96 KB or more per SM are on the way, twice
-// what the memory's latency needs at its full rate (registers as the
-// destination, 32 KB per SM, gave 228 us where the ring gave 147, on 682 MB; a
-// range per CTA instead of per warp, its warps' sums merged at each segment's
-// end, left the SMs idle for a third of that: 116 us now, 5.9 TB/s).  The 16 tokens are the rows of
-// S^T = K Q^T, 16 values of d are the rows of O^T = V^T P^T (both mma.sync
-// m16n8k16), and 8 query heads are the columns of both, so a group of up to 8
-// heads wastes nothing that costs.  The order of d inside a product is free,
+// in flight while it works on one: up to 8 heads to a KV head 128 KB or more per
+// SM are on the way (160 at D = 64), more than twice what the memory's latency
+// needs at its full rate; with 9 to 16 heads one CTA fits an SM, and 80 KB (D = 64),
+// 64 KB (128) and 128 KB (256) are.  (Registers as the destination, 32 KB per SM,
+// gave 228 us where the ring gave 147, on 682 MB; a range per CTA instead of per
+// warp, its warps' sums merged at each segment's end, left the SMs idle for a third
+// of that: 121 us now, 5.6 TB/s.)  The 16 tokens are the rows of S^T = K Q^T, 16
+// values of d are the rows of O^T = V^T P^T (both mma.sync m16n8k16), and 8 query
+// heads are the columns of both, so a group of up to 8 heads wastes nothing that
+// costs.  A second tile of 8 heads doubles the operands in registers: at D = 256 the
+// kernel spills (184 B stored and 320 B read per thread at 255 registers), and 64
+// sequences of up to 16384 tokens on 4 KV heads take 268 us with 16 heads to each
+// where 8 take 121; at D = 128, 8 KV heads, nothing spills: 148 us against 121.  The order of d inside a product is free,
 // so each lane's 16 bytes of one token (16 codes) are its operand as they
 // stand; for V the codes of two tokens are interleaved by byte permutes.  The
 // copies place 16-byte pieces so that both reads are free of bank conflicts.
@@ -443,7 +448,8 @@ __global__ void __launch_bounds__(W * 32, D == 256 || NT == 2 ? 1 : 2) kv8_decod
     // 32768 22.2 / 26.2; 8 of 8192, 1 head, 13.1 / 17.6; 4 of 16384, 8 heads,
     // 32.0 / 34.2; with units of 64 tokens 24.0, 25.4, 17.5 and 33.9.
     // Otherwise neighbours in the order are on different SMs, and there is a worker
-    // for each unit up to 512 and then one for 256 tokens until every warp has work.
+    // for every two units up to 512 workers, and more only from where each has 256
+    // tokens, until every warp has work.
     const long long all = min((long long)gridDim.x * W, U) / W * W;
     const bool groups = all >= 2LL * W * a.B * a.Hkv;
     const long long C = groups ? all : min((long long)gridDim.x * W, max(min((U * TILE + 63) / 64, 512LL), U * TILE / 256));
@@ -873,8 +879,9 @@ int split_workers(int B, int Hq, int Hkv, int D, int T, int maxp) {
 // 152, 30.1 / 19.5 for 600; of 4096 tokens 10.2 / 8.4, 35.9 / 28.0, 121.4 / 95.8
 // where all are full and 10.6 / 7.6, 24.1 / 34.7, 73.3 / 63.7 where their lengths
 // are spread.  The pair kernel's lead shrinks with the length (one pair: 3.1 us at
-// 512, 1.8 at 4096) and is lost at 152 spread pairs, so the split kernel takes
-// over above 4096.
+// 512, 1.8 at 4096), so the split kernel takes over above 4096.  Below it the rule
+// looks at the table's width only, and takes the slower kernel where a pair has one
+// CTA and few of many sequences are long (24.1 / 34.7): the longest one is the time.
 int pair_ctas(int B, int Hkv, int T, int maxp) {
     const long long cap = (long long)maxp * T, pairs = (long long)B * Hkv;
     if (cap > PAIR_TOKENS) return 0;

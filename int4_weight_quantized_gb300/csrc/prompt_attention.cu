@@ -21,17 +21,19 @@
 // holding one row: maximum, 2^x, sum, and P as fp16.  What overlaps, and what
 // tensor memory's 512 columns hold, goes by D:
 //   128: two tiles per CTA; the tensor cores work on one while the other's
-//        softmax runs; P lies over its S.  16384 tokens, 16 heads on 2: 669 us,
-//        1640 TFLOP/s; the softmax of a tile takes 1100 cycles beside the 1024
-//        of its two products, and power sets the clock.
+//        softmax runs; P lies over its S.  16384 tokens, 16 heads on 2: 731-738 us,
+//        1490-1504 TFLOP/s; the softmax of a tile takes 1100 cycles beside the 1024
+//        of its two products, and power sets the clock (669 us was measured once).  At
+//        168 registers 16 B are spilled and 36 B read back per thread.
 //   256: one tile, S twice: the next S is computed ahead.  8192 tokens, 8 heads
-//        on 1: 1627 TFLOP/s under ncu.
+//        on 1: 184 us, 1490 TFLOP/s (1608 under ncu).
 //   64:  one tile, two CTAs per SM, P beside S: the next S waits only until
 //        this one has been read.  The softmax sets the pace (1030 cycles per
 //        tile and SM beside 512 of products and 512 of the 2^x pipe): 12
 //        sequences of 93-2500 tokens, 24 heads on 8, 111 us.
-// (8 warps per tile, two threads to a row, were slower: 132 us and, at D = 128,
-// 817: what issues the products shares a quarter of the SM with them.)
+// (8 warps per tile, two threads to a row, were slower: 132 us against 111 and, at
+// D = 128, 817 against 669: what issues the products shares a quarter of the SM
+// with them.)
 // O stays in tensor memory for the whole pass; it is rescaled
 // only when a row's maximum has grown by more than 2^8 since the one in use,
 // which after the first tiles is rare.  m is 7 below that maximum, so that p at
@@ -48,7 +50,9 @@
 //   - on the diagonal some rows of a tile see a key and others do not: V's rows
 //     there are looked through, an inf or a NaN (which a working model has not)
 //     becomes zero and its key is noted, and the rows that do see the key get
-//     its value added at the end.
+//     its value added at the end.  At D = 256 this comes after S and the last
+//     step's product (prompt_ring.h says why): 512 tokens, 8 heads on 1, take 11.6
+//     us with these waits.
 #include <cuda.h>
 #include <math.h>
 
