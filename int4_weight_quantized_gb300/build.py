@@ -9,6 +9,7 @@ built whatever becomes of the module; where that does not build, the calls that
 need it say why.  Rebuilds only when a source or header is newer than what was
 built, and the module also for another torch.
 """
+import contextlib
 import glob
 import json
 import os
@@ -124,12 +125,13 @@ def _finish_binding(compiled):
         _link_binding(compiled.result())
     except Exception as e:                       # whatever it is, the library is there
         error = str(e) or repr(e)
-        if os.path.exists(EXT):                  # of older sources, or of another torch
+        with contextlib.suppress(FileNotFoundError):     # of older sources, or of another torch
             os.remove(EXT)
         warnings.warn("the Python module of prompt attention and the 8-bit cache was not built: " + error)
-    with open(STAMP + ".tmp", "w") as f:
+    fd, tmp = tempfile.mkstemp(suffix=".json", dir=OUT_DIR)
+    with os.fdopen(fd, "w") as f:
         json.dump({"torch": _torch_id(), "error": error}, f)
-    os.replace(STAMP + ".tmp", STAMP)
+    os.replace(tmp, STAMP)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:

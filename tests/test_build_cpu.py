@@ -77,6 +77,19 @@ def test_another_torch_gets_a_module_of_its_own(tree, monkeypatch):
     assert len(cpp) == 3 and os.path.exists(B.EXT)
 
 
+def test_builds_side_by_side_note_their_module(tree, monkeypatch):
+    # as parallel test workers do: nobody takes the file that another is writing
+    from concurrent.futures import Future, ThreadPoolExecutor
+    os.makedirs(B.OUT_DIR)
+    done = Future()
+    done.set_result("binding.o")
+    monkeypatch.setattr(B, "_link_binding", _module)
+    with ThreadPoolExecutor(8) as ex:
+        for f in [ex.submit(B._finish_binding, done) for _ in range(200)]:
+            f.result()
+    assert json.load(open(B.STAMP))["error"] == "" and os.listdir(B.OUT_DIR) in (["_w4a8.so", "_w4a8.json"], ["_w4a8.json", "_w4a8.so"])
+
+
 def test_a_library_that_does_not_compile_is_an_error(tree, monkeypatch):
     (tree / "csrc" / "one.cu").write_text("#error broken\n")
     with pytest.raises(RuntimeError, match="broken"):
