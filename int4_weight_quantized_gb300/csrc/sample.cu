@@ -12,23 +12,24 @@
 //
 // Nothing is sorted.  fp16 logits have at most 65536 values, so a row is its counts
 // per value, integers that no order of summation changes; a weight is computed once
-// per value, not per word, in 64 bits.  The sums from the order's beginning are
-// prefix sums over the values, and the word is found as "the i-th with value v".
+// per value, not per word, to 2^-40 of itself (weight.h).  The sums from the order's
+// beginning are prefix sums over the values, and the word is found as "the i-th with value v".
 //
 // A cluster of CTAs takes a row, each a range of the words, which stay in registers: it
-// counts them in shared memory (16 bits a value, 128 KB), weighs the counts (weight.h) and
-// adds the sums of groups of 32 values and of binades of 1024, as integers, to those in the
-// first CTA; the first warp there looks the borders up in them; the CTA that has the word
-// finds it.  (A share of the values for each CTA, summed over all CTAs' counts, was a
+// counts them in shared memory (16 bits a value, 128 KB), multiplies the counts of each group
+// of 32 values by the weights relative to the group's first value and adds the sums, integers,
+// to those in the first CTA; that one multiplies them by the first values' weights, and its
+// first warp looks the borders up in them; the CTA that has the word finds it.  (Rounded in
+// each CTA, a group's sum would depend on how the words are dealt out.  A share of the values for each CTA, summed over all CTAs' counts, was a
 // third of the time: shared memory of other CTAs is read at 10 bytes a cycle.)
 //
 // What bounds it: a CTA's chain of phases, one CTA to an SM.  256 rows of 262144 words, 4
-// CTAs to a row, take 163 us, 36 rows at once (the words alone, 134 MB, 20): clearing the
+// CTAs to a row, take 172 us, 36 rows at once (the words alone, 134 MB, 20): clearing the
 // counts 1 us, the words' way here 3, counting 65536 words 5.5 (a warp's addition to shared
 // memory takes 4.9 cycles), weights 4.5, looking the borders up 2 and 1 to 1.5 a filter (min-p beside the others),
 // finding the word 0.5 to 2, three barriers of the cluster 0.8 each.  64 rows of 131072, 2 CTAs each:
-// 21.4 us; one of 32000, 8 CTAs: 13.4.  More CTAs to a row than its words need are
-// taken while all rows' are resident together: 8 for one row of 32000 words 13.4 us where
+// 22.4 us; one of 32000, 8 CTAs: 12.8.  More CTAs to a row than its words need are
+// taken while all rows' are resident together: 8 for one row of 32000 words 12.8 us where
 // one would count 32000 words alone.  The words stay in registers: read again for the last
 // phase, 256 rows took 185 us instead of 169.
 #include <math.h>
@@ -51,7 +52,8 @@ constexpr int kGroups = kValues / 32, kBinades = kValues / 1024;
 constexpr int kLast = 0xFBFF;                    // the lowest finite value (-inf, a masked word, and NaNs are not counted)
 constexpr int kVectors = 8 * NT;                 // vectors of 8 words that a CTA takes: 65536 words
 constexpr int kCluster = 8;
-constexpr float kUnit = 0x1p44f;                 // sums of weights are integers, of 2^-44: up to 2^63 for 2^19 words
+constexpr int kUnits = 18;                       // sums of weights are integers, of 2^(18 - 62): up to 2^63 for 2^19 words
+constexpr float kUnit = 0x1p44f;
 
 // The places of two fp16 values in the order: 0x7FFF - h from 0 up (0x7FFF ^ h), h below.
 // (h + 0 is h, but for -0, which becomes 0.)
@@ -113,14 +115,12 @@ __device__ __forceinline__ void add_dsmem_u64(uint32_t addr, unsigned long long 
 
 struct Shared {
     uint32_t count[kValues / 2];                 // two values a word
-    // in the first CTA: the groups' and the binades' counts and weights, summed over the CTAs
-    unsigned long long mass[kGroups], mass_q[kBinades];
+    // in the first CTA: the groups' and the binades' counts and weights, summed over the CTAs.
+    // A group's weight comes in two sums, of the high and of the low 32 bits of its values'.
+    unsigned long long mass[kGroups], rest[kGroups], mass_q[kBinades];
     uint32_t words[kGroups], words_q[kBinades];
     weight::Pair table[weight::kSteps];
-    // by binade: the weights of k values' distance, in 2^-47, and of 32 k values', in 2^-63
-    alignas(16) unsigned long long step1[32][32];
-    unsigned long long step32[32][32];
-    unsigned long long base[kBinades];     // the weight of the first of 1024 values, in 2^-63
+    alignas(16) unsigned long long step[32][32];     // by binade: the weight of k values' distance, in 2^-63
     int top, bottom;                             // smallest and largest place that this CTA has seen
     int extra;                                   // the place of a word that is not in count, or -1
     int extras[kCluster];                        // all CTAs'
@@ -142,12 +142,8 @@ __global__ void __launch_bounds__(NT, 1) sample_kernel(const SampleArgs a, int C
     const int rank = (int)(blockIdx.x % (unsigned)CL), b = (int)(blockIdx.x / (unsigned)CL);
     for (int i = tid; i < kValues / 8; i += NT) reinterpret_cast<uint4 *>(sm.count)[i] = make_uint4(0u, 0u, 0u, 0u);
     for (int i = tid; i < kGroups; i += NT) {
-        sm.mass[i] = 0;
+        sm.mass[i] = sm.rest[i] = 0;
         sm.words[i] = 0;
-    }
-    if (tid < kBinades) {
-        sm.mass_q[tid] = 0;
-        sm.words_q[tid] = 0;
     }
     if (tid < weight::kSteps) sm.table[tid] = weight::kPowers[tid];
     if (tid == 0) {
@@ -198,9 +194,7 @@ __global__ void __launch_bounds__(NT, 1) sample_kernel(const SampleArgs a, int C
     r.table = sm.table;
     if (!greedy) {
         // (distances in binade e: 2^(e - 25), the lowest two alike)
-        const float d = ldexpf(-(float)lane, max(warp, 1) - 25);
-        sm.step1[warp][lane] = weight::fixed(weight::of(d, 0.0f, r.slope, r.table), 47);
-        sm.step32[warp][lane] = weight::fixed(weight::of(32.0f * d, 0.0f, r.slope, r.table), 63);
+        sm.step[warp][lane] = weight::fixed(weight::of(ldexpf(-(float)lane, max(warp, 1) - 25), 0.0f, r.slope, r.table));
     }
     // (65536 words of one value would not fit its count: a full CTA's last word is kept apart)
     const bool full = NV == 8 && share == kVectors && tid == NT - 1;
@@ -249,19 +243,22 @@ __global__ void __launch_bounds__(NT, 1) sample_kernel(const SampleArgs a, int C
     const int extra = sm.extra;
     r.top = none ? 0.0f : value_at(r.first);
     const int q0 = r.first / 1024, q1 = bottom / 1024;
-    if (tid > q0 && tid <= q1 && !greedy) sm.base[tid] = weight::fixed(r.at(tid * 1024), 63);
-    __syncthreads();
 
     // sums of counts and of weights of the groups: a warp takes a binade's 1024 values, a
-    // lane a group of 32.  They lie at equal distances: the k-th of a group weighs step1[k]
-    // times the first.
+    // lane a group of 32.  They lie at equal distances: the k-th of a group weighs step[k]
+    // times the first.  What the CTAs add up is integers that nothing has been cut from, so
+    // it is the same however the words are dealt out.
     if (!none && !greedy) {
         for (int q = q0 + warp; q <= q1; q += NT / 32) {
             const int e = q < 32 ? 31 - q : q - 32, d0 = q * 1024 + lane * 32;
-            // (before the largest value nothing is counted)
+            // before the largest value nothing is counted
             const int k0 = max(0, r.first - d0);
             uint32_t words = 0;
-            unsigned long long sum = 0;                      // (no more than 2^16 words)
+            unsigned long long high = 0, low = 0;            // (no more than 2^16 words)
+            auto weigh = [&](uint32_t c, unsigned long long w) {
+                high += (unsigned long long)c * (uint32_t)(w >> 32);
+                low += (unsigned long long)c * (uint32_t)w;
+            };
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 // (the order differs by lane: no two of 8 lanes meet in a bank)
@@ -274,37 +271,46 @@ __global__ void __launch_bounds__(NT, 1) sample_kernel(const SampleArgs a, int C
                 if (q > q0) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const ulonglong2 w = *reinterpret_cast<const ulonglong2 *>(&sm.step1[e][8 * v + 2 * k]);
-                        sum += c[2 * k] * w.x + c[2 * k + 1] * w.y;
+                        const ulonglong2 w = *reinterpret_cast<const ulonglong2 *>(&sm.step[e][8 * v + 2 * k]);
+                        weigh(c[2 * k], w.x);
+                        weigh(c[2 * k + 1], w.y);
                     }
                 } else {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) sum += c[k] * sm.step1[e][max(0, 8 * v + k - k0)];
+                    for (int k = 0; k < 8; ++k) weigh(c[k], sm.step[e][max(0, 8 * v + k - k0)]);
                 }
             }
             if (NV == 8 && extra >> 5 == d0 >> 5) {
                 ++words;
-                sum += sm.step1[e][max(0, extra - d0 - k0)];
+                weigh(1u, sm.step[e][max(0, extra - d0 - k0)]);
             }
-            const uint32_t in_all = __reduce_add_sync(0xffffffffu, words);
-            if (in_all == 0) continue;
-            // (in 2^-62)
-            const unsigned long long first = q > q0 ? __umul64hi(sm.step32[e][lane], sm.base[q]) : weight::fixed(r.at(max(d0, r.first)), 62);
-            const unsigned long long m = words ? (__umul64hi(sum, first) + 1) >> 1 : 0;      // 2^-45 to units
             if (words) {
                 add_dsmem_u32(dsmem_addr(smem_u32(&sm.words[d0 / 32]), 0u), words);
-                add_dsmem_u64(dsmem_addr(smem_u32(&sm.mass[d0 / 32]), 0u), m);
-            }
-            // (22 bits at a time: m is below 2^61)
-            const uint32_t m0 = __reduce_add_sync(0xffffffffu, (uint32_t)m & 0x3FFFFFu), m1 = __reduce_add_sync(0xffffffffu, (uint32_t)(m >> 22) & 0x3FFFFFu);
-            const uint32_t m2 = __reduce_add_sync(0xffffffffu, (uint32_t)(m >> 44));
-            if (lane == 0) {
-                add_dsmem_u32(dsmem_addr(smem_u32(&sm.words_q[q]), 0u), in_all);
-                add_dsmem_u64(dsmem_addr(smem_u32(&sm.mass_q[q]), 0u), ((unsigned long long)m2 << 44) + ((unsigned long long)m1 << 22) + m0);
+                add_dsmem_u64(dsmem_addr(smem_u32(&sm.mass[d0 / 32]), 0u), high);
+                add_dsmem_u64(dsmem_addr(smem_u32(&sm.rest[d0 / 32]), 0u), low);
             }
         }
     }
     cluster_sync_all();
+
+    // the groups' weights in units, and the binades' sums: a warp to a binade, a lane to a group
+    if (rank == 0 && !none && !greedy) {
+        for (int q = warp; q < kBinades; q += NT / 32) {
+            const int g = q * 32 + lane;
+            const uint32_t words = sm.words[g], in_all = __reduce_add_sync(0xffffffffu, words);
+            unsigned long long m = 0;
+            if (words) m = weight::units_of_group(sm.mass[g], sm.rest[g], r.at(max(g * 32, r.first)), kUnits);
+            sm.mass[g] = m;
+            // (22 bits at a time: m is below 2^63)
+            const uint32_t m0 = __reduce_add_sync(0xffffffffu, (uint32_t)m & 0x3FFFFFu), m1 = __reduce_add_sync(0xffffffffu, (uint32_t)(m >> 22) & 0x3FFFFFu);
+            const uint32_t m2 = __reduce_add_sync(0xffffffffu, (uint32_t)(m >> 44));
+            if (lane == 0) {
+                sm.words_q[q] = in_all;
+                sm.mass_q[q] = ((unsigned long long)m2 << 44) + ((unsigned long long)m1 << 22) + m0;
+            }
+        }
+        __syncthreads();
+    }
 
     int chosen = 0;                              // in the first CTA's first warp: the word's value, the weight of all kept
     unsigned long long kept = 0;

@@ -113,12 +113,24 @@ W_FN Pair pair_of(Weight w) {
     return {mul(w.h, scale.f), mul(w.l, scale.f)};
 }
 
-// A weight of at most 1 in units of 2^-bits, cut (bits from 47 on).
-W_FN uint64_t fixed(Weight w, int bits) {
-    // h is a multiple of 2^-24
-    const uint64_t m = ((uint64_t)(uint32_t)mul(w.h, 0x1p24f) << 24) + (uint64_t)(int64_t)(int32_t)rintf(mul(w.l, 0x1p48f));
-    const int by = bits - 48 + w.n;
+// A weight's h + l in units of 2^-48 (h is a multiple of 2^-24).
+W_FN uint64_t mantissa(Weight w) { return ((uint64_t)(uint32_t)mul(w.h, 0x1p24f) << 24) + (uint64_t)(int64_t)(int32_t)rintf(mul(w.l, 0x1p48f)); }
+
+// A weight of at most 1 in units of 2^-63, cut.
+W_FN uint64_t fixed(Weight w) {
+    const uint64_t m = mantissa(w);
+    const int by = 15 + w.n;
     return by >= 0 ? m << by : by > -64 ? m >> -by : 0;
+}
+
+// The weight of a group of words, whose sum of count * fixed(weight relative to the group's
+// first value) is high 2^32 + low and whose first value weighs `first`, in units of
+// 2^(e - 62), cut once.  (Words number up to 2^19, so high is below 2^51.)
+W_FN uint64_t units_of_group(uint64_t high, uint64_t low, Weight first, int e) {
+    const uint64_t m = mantissa(first);
+    const unsigned __int128 s = (unsigned __int128)high * m + (((unsigned __int128)low * m) >> 32);      // 2^(first.n - 79)
+    const int by = 17 - first.n + e;
+    return by < 128 ? (uint64_t)(s >> by) : 0;
 }
 
 // a += count w
