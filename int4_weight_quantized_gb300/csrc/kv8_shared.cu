@@ -532,6 +532,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_shared_kernel(const SharedArgs
                 uint32_t sr[HK];
                 float *x = reinterpret_cast<float *>(sr);
                 const bool cut = all_see - key0 < KT;
+                if (cut) {
+                    // (an infinite scale of a block that others see would make NaN of -inf)
+#pragma unroll
+                    for (int i = 0; i < NB; ++i) lw[i] = 16 * i < limit - key0 ? lw[i] : -INFINITY;
+                }
                 auto load = [&](int h) {                             // scores of the h-th HK keys
 #pragma unroll
                     for (int i = 0; i < HK / 32; ++i) tmem_ld_cols<32>(base + (uint32_t)(buf * KT + h * HK + 32 * i), sr + 32 * i);
