@@ -404,7 +404,8 @@ w4a8_status w4a8_kv8_extend(int32_t *table, int32_t *lens, const int32_t *add, i
  * beginning passes u[b] M, logprobs[b] = ln(w_j / M).  Where T is not above 0 the
  * first word alone is kept.  NaN and -inf are never chosen; a row of nothing else
  * gets token -1 and logprob -inf.  Beside +inf everything else has weight 0.
- * Weights and sums in 64 bits.  The settings may be NULL (T = 1, no filter), as may
+ * A weight is computed to 2^-40 of itself, M and the sums from the beginning to 2^-39 of
+ * themselves, and a row's results are the same in every batch.  The settings may be NULL (T = 1, no filter), as may
  * logprobs.  u, settings and results are [B], device, 4-byte aligned; logits are
  * 2-byte aligned.  Requires ld >= V, or ld = 0 (one row of
  * logits for all), 1 <= V <= 524272 (W4A8_ERR_UNSUPPORTED above);

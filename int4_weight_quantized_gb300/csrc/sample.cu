@@ -18,9 +18,11 @@
 // A cluster of CTAs takes a row, each a range of the words, which stay in registers: it
 // counts them in shared memory (16 bits a value, 128 KB), multiplies the counts of each group
 // of 32 values by the weights relative to the group's first value and adds the sums, integers,
-// to those in the first CTA; that one multiplies them by the first values' weights, and its
-// first warp looks the borders up in them; the CTA that has the word finds it.  (Rounded in
-// each CTA, a group's sum would depend on how the words are dealt out.  A share of the values for each CTA, summed over all CTAs' counts, was a
+// to those in the first CTA; that one multiplies them by the first values' weights and puts
+// them into units of 2^-59 or less of their sum, and its first warp looks the borders up in
+// them; the CTA that has the word finds it.  (Rounded in each CTA, a group's sum would depend
+// on how the words are dealt out; with units of 2^-44 of the first word numbers next to 1 drew
+// a neighbour of the word that they stand for: 2^19 words of 2^-41 are 2^-22 of a row.  A share of the values for each CTA, summed over all CTAs' counts, was a
 // third of the time: shared memory of other CTAs is read at 10 bytes a cycle.)
 //
 // What bounds it: a CTA's chain of phases, one CTA to an SM.  256 rows of 262144 words, 4
@@ -28,8 +30,8 @@
 // counts 1 us, the words' way here 3, counting 65536 words 5.5 (a warp's addition to shared
 // memory takes 4.9 cycles), weights 4.5, looking the borders up 2 and 1 to 1.5 a filter (min-p beside the others),
 // finding the word 0.5 to 2, three barriers of the cluster 0.8 each.  64 rows of 131072, 2 CTAs each:
-// 22.4 us; one of 32000, 8 CTAs: 12.8.  More CTAs to a row than its words need are
-// taken while all rows' are resident together: 8 for one row of 32000 words 12.8 us where
+// 22.5 us; one of 32000, 8 CTAs: 13.5.  More CTAs to a row than its words need are
+// taken while all rows' are resident together: 8 for one row of 32000 words 13.5 us where
 // one would count 32000 words alone.  The words stay in registers: read again for the last
 // phase, 256 rows took 185 us instead of 169.
 #include <math.h>
@@ -52,8 +54,6 @@ constexpr int kGroups = kValues / 32, kBinades = kValues / 1024;
 constexpr int kLast = 0xFBFF;                    // the lowest finite value (-inf, a masked word, and NaNs are not counted)
 constexpr int kVectors = 8 * NT;                 // vectors of 8 words that a CTA takes: 65536 words
 constexpr int kCluster = 8;
-constexpr int kUnits = 18;                       // sums of weights are integers, of 2^(18 - 62): up to 2^63 for 2^19 words
-constexpr float kUnit = 0x1p44f;
 
 // The places of two fp16 values in the order: 0x7FFF - h from 0 up (0x7FFF ^ h), h below.
 // (h + 0 is h, but for -0, which becomes 0.)
@@ -80,22 +80,22 @@ struct Row {
         return weight::of(value_at(d), top, slope, table);
     }
 };
-// A sum of weights in units.
-__device__ __forceinline__ unsigned long long units_of(weight::Pair a) {
-    return __float2ull_rn(a.h * kUnit) + (unsigned long long)__float2ll_rn(a.l * kUnit);
+// A sum of weights in units (of which there are so many to 1).
+__device__ __forceinline__ unsigned long long units_of(weight::Pair a, float units) {
+    return __float2ull_rn(a.h * units) + (unsigned long long)__float2ll_rn(a.l * units);
 }
 
 // How many of the words i = 0 .. c - 1 of weight w have less than `border` units in the i
 // words before them.  (The quotient is off by 2^-22 of up to 2^19 words: by one.)
-__device__ __forceinline__ uint32_t words_below(unsigned long long border, uint32_t c, weight::Weight w) {
+__device__ __forceinline__ uint32_t words_below(unsigned long long border, uint32_t c, weight::Weight w, float units) {
     auto before = [&](uint32_t i) {
         weight::Pair s = {0.0f, 0.0f};
         weight::accumulate(s, (float)i, w);
-        return units_of(s);
+        return units_of(s, units);
     };
     weight::Pair one = {0.0f, 0.0f};
     weight::accumulate(one, 1.0f, w);
-    const float q = ceilf(__ull2float_rn(border) / (one.h * kUnit));
+    const float q = ceilf(__ull2float_rn(border) / (one.h * units));
     uint32_t n = q < (float)c ? (uint32_t)q : c;             // (c where the weight is 0)
     while (n < c && before(n) < border) ++n;
     while (n > 0 && before(n - 1) >= border) --n;
@@ -121,6 +121,8 @@ struct Shared {
     uint32_t words[kGroups], words_q[kBinades];
     weight::Pair table[weight::kSteps];
     alignas(16) unsigned long long step[32][32];     // by binade: the weight of k values' distance, in 2^-63
+    uint16_t step_next[32][32];                      // and its next 11 bits
+    uint32_t total[NT / 32];                         // by warp: the weight of its groups, roughly
     int top, bottom;                             // smallest and largest place that this CTA has seen
     int extra;                                   // the place of a word that is not in count, or -1
     int extras[kCluster];                        // all CTAs'
@@ -194,7 +196,9 @@ __global__ void __launch_bounds__(NT, 1) sample_kernel(const SampleArgs a, int C
     r.table = sm.table;
     if (!greedy) {
         // (distances in binade e: 2^(e - 25), the lowest two alike)
-        sm.step[warp][lane] = weight::fixed(weight::of(ldexpf(-(float)lane, max(warp, 1) - 25), 0.0f, r.slope, r.table));
+        const weight::Weight w = weight::of(ldexpf(-(float)lane, max(warp, 1) - 25), 0.0f, r.slope, r.table);
+        sm.step[warp][lane] = weight::fixed(w);
+        sm.step_next[warp][lane] = (uint16_t)weight::fixed_next(w);
     }
     // (65536 words of one value would not fit its count: a full CTA's last word is kept apart)
     const bool full = NV == 8 && share == kVectors && tid == NT - 1;
@@ -284,6 +288,14 @@ __global__ void __launch_bounds__(NT, 1) sample_kernel(const SampleArgs a, int C
                 ++words;
                 weigh(1u, sm.step[e][max(0, extra - d0 - k0)]);
             }
+            if (weight::is_steep(sm.step[e][31]) && words) {
+                low <<= 11;
+#pragma unroll 1
+                for (int k = 0; k < 32; ++k) {
+                    const uint32_t two = sm.count[(d0 + k) / 2];
+                    low += ((k & 1 ? two >> 16 : two & 0xFFFFu) + (NV == 8 && extra == d0 + k)) * sm.step_next[e][max(0, k - k0)];
+                }
+            }
             if (words) {
                 add_dsmem_u32(dsmem_addr(smem_u32(&sm.words[d0 / 32]), 0u), words);
                 add_dsmem_u64(dsmem_addr(smem_u32(&sm.mass[d0 / 32]), 0u), high);
@@ -293,15 +305,36 @@ __global__ void __launch_bounds__(NT, 1) sample_kernel(const SampleArgs a, int C
     }
     cluster_sync_all();
 
-    // the groups' weights in units, and the binades' sums: a warp to a binade, a lane to a group
+    // The groups' weights, and the binades' sums: a warp to a binade, a lane to a group.  They
+    // are integers in units of 2^-59 or less of the sum of all.
+    float units = 1.0f;
     if (rank == 0 && !none && !greedy) {
-        for (int q = warp; q < kBinades; q += NT / 32) {
-            const int g = q * 32 + lane;
-            const uint32_t words = sm.words[g], in_all = __reduce_add_sync(0xffffffffu, words);
-            unsigned long long m = 0;
-            if (words) m = weight::units_of_group(sm.mass[g], sm.rest[g], r.at(max(g * 32, r.first)), kUnits);
+        constexpr int QW = kBinades / (NT / 32);
+        weight::Sum of[QW];
+        uint32_t words[QW], total = 0;
+#pragma unroll
+        for (int i = 0; i < QW; ++i) {
+            const int q = warp + i * (NT / 32), g = q * 32 + lane;
+            of[i] = {0, 0};
+            words[i] = sm.words[g];
+            if (words[i]) {
+                const unsigned long long low = sm.rest[g];
+                of[i] = weight::weight_of_group(sm.mass[g], weight::is_steep(sm.step[q < 32 ? 31 - q : q - 32][31]) ? low >> 11 : low, r.at(max(g * 32, r.first)));
+            }
+            total += weight::roughly(of[i]);
+        }
+        total = __reduce_add_sync(0xffffffffu, total);
+        if (lane == 0) sm.total[warp] = total;
+        __syncthreads();
+        const int e = weight::units_for(__reduce_add_sync(0xffffffffu, sm.total[lane]));
+        units = __uint_as_float((uint32_t)(62 - e + 127) << 23);
+#pragma unroll
+        for (int i = 0; i < QW; ++i) {
+            const int q = warp + i * (NT / 32), g = q * 32 + lane;
+            const unsigned long long m = weight::in_units(of[i], e);
             sm.mass[g] = m;
-            // (22 bits at a time: m is below 2^63)
+            const uint32_t in_all = __reduce_add_sync(0xffffffffu, words[i]);
+            // (22 bits at a time)
             const uint32_t m0 = __reduce_add_sync(0xffffffffu, (uint32_t)m & 0x3FFFFFu), m1 = __reduce_add_sync(0xffffffffu, (uint32_t)(m >> 22) & 0x3FFFFFu);
             const uint32_t m2 = __reduce_add_sync(0xffffffffu, (uint32_t)(m >> 44));
             if (lane == 0) {
@@ -378,7 +411,7 @@ __global__ void __launch_bounds__(NT, 1) sample_kernel(const SampleArgs a, int C
                 if (p < CL) v.c += (d & 1 ? w[p] >> 16 : w[p] & 0xFFFFu) + (NV == 8 && sm.extras[p] == d);
             weight::Pair one = {0.0f, 0.0f};
             if (v.c) weight::accumulate(one, (float)v.c, v.w);
-            const Sums s = scan(v.c, units_of(one), __shfl_sync(0xffffffffu, in.before, l), __shfl_sync(0xffffffffu, in.mass_before, l));
+            const Sums s = scan(v.c, units_of(one, units), __shfl_sync(0xffffffffu, in.before, l), __shfl_sync(0xffffffffu, in.mass_before, l));
             v.before = s.before;
             v.mass = s.mass_before;
             return v;
@@ -393,7 +426,7 @@ __global__ void __launch_bounds__(NT, 1) sample_kernel(const SampleArgs a, int C
             // (where the last of them lies; nothing of the group: what is before it)
             weight::Pair some = {0.0f, 0.0f};
             if (c) weight::accumulate(some, (float)c, v.w);
-            const unsigned long long m = v.mass + units_of(some);
+            const unsigned long long m = v.mass + units_of(some, units);
             const unsigned any = __ballot_sync(0xffffffffu, c);
             M = __shfl_sync(0xffffffffu, m, any ? 31 - __clz(any) : 0);
         };
@@ -408,7 +441,7 @@ __global__ void __launch_bounds__(NT, 1) sample_kernel(const SampleArgs a, int C
             const double t = (double)p * (double)M;
             const unsigned long long border = t > 0.0 ? (unsigned long long)__double2ull_ru(t) : 0ull;
             const Values v = look([&](int, uint32_t, unsigned long long units) { return units < border; });
-            keep(v, v.c && v.mass < border ? words_below(border - v.mass, v.c, v.w) : 0u);
+            keep(v, v.c && v.mass < border ? words_below(border - v.mass, v.c, v.w, units) : 0u);
         }
         if (pm > 0.0f && warp == 1) {
             // words whose weight is min_p or more
@@ -429,7 +462,7 @@ __global__ void __launch_bounds__(NT, 1) sample_kernel(const SampleArgs a, int C
         }
         if (n == 0) {
             n = 1;
-            M = units_of({1.0f, 0.0f});
+            M = units_of({1.0f, 0.0f}, units);
         }
         if (warp == 0) {
             float u = sm.u;
@@ -440,7 +473,7 @@ __global__ void __launch_bounds__(NT, 1) sample_kernel(const SampleArgs a, int C
             const unsigned some = __ballot_sync(0xffffffffu, v.c && v.before < n), any = __ballot_sync(0xffffffffu, v.c && v.before < n && v.mass <= border);
             const int l = any ? 31 - __clz(any) : some ? __ffs(some) - 1 : 0;
             // (of its value's words, those before which no more than the rest of t lies)
-            const uint32_t past = some && v.mass <= border ? words_below(border - v.mass + 1, min(v.c, n - v.before), v.w) : 0u;
+            const uint32_t past = some && v.mass <= border ? words_below(border - v.mass + 1, min(v.c, n - v.before), v.w, units) : 0u;
             if (lane == l) {
                 sm.place = some ? v.g * 32 + lane : r.first;
                 sm.nth = past > 0 ? past - 1 : 0u;
@@ -460,7 +493,7 @@ __global__ void __launch_bounds__(NT, 1) sample_kernel(const SampleArgs a, int C
         if (kept) {
             // (what is over is exact: 24 bits of 64 are gone)
             const float h = __ull2float_rn(kept), l = __ll2float_rn((long long)(kept - __float2ull_rn(h)));
-            logp = weight::log_share(value_at(chosen), r.top, temp, {h / kUnit, l / kUnit}, r.table);
+            logp = weight::log_share(value_at(chosen), r.top, temp, {h / units, l / units}, r.table);
         }
         a.logprobs[b] = logp;
     }

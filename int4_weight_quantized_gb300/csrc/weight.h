@@ -116,21 +116,57 @@ W_FN Pair pair_of(Weight w) {
 // A weight's h + l in units of 2^-48 (h is a multiple of 2^-24).
 W_FN uint64_t mantissa(Weight w) { return ((uint64_t)(uint32_t)mul(w.h, 0x1p24f) << 24) + (uint64_t)(int64_t)(int32_t)rintf(mul(w.l, 0x1p48f)); }
 
-// A weight of at most 1 in units of 2^-63, cut.
-W_FN uint64_t fixed(Weight w) {
+// A weight of at most 1 in units of 2^-63, cut, and the 11 bits that come next.
+W_FN uint64_t cut(Weight w, int bits) {
     const uint64_t m = mantissa(w);
-    const int by = 15 + w.n;
+    const int by = bits - 48 + w.n;
     return by >= 0 ? m << by : by > -64 ? m >> -by : 0;
 }
+W_FN uint64_t fixed(Weight w) { return cut(w, 63); }
+W_FN uint32_t fixed_next(Weight w) { return (uint32_t)cut(w, 74) & 2047u; }
 
-// The weight of a group of words, whose sum of count * fixed(weight relative to the group's
-// first value) is high 2^32 + low and whose first value weighs `first`, in units of
-// 2^(e - 62), cut once.  (Words number up to 2^19, so high is below 2^51.)
-W_FN uint64_t units_of_group(uint64_t high, uint64_t low, Weight first, int e) {
+// Words of a group of 32 neighbouring values are summed as count * fixed(their weight
+// relative to the group's first value): high 2^32 + low, words numbering up to 2^19.  Where
+// the last of the 32 is below 2^-22 the next bits count too, low being in units of 2^-74:
+// 2^19 words of 2^-43, the smallest that a number of 24 bits reaches among so many, are
+// off by 2^-55 together.
+W_FN bool is_steep(uint64_t last) { return last < (1ull << 41); }
+
+// A sum m 2^n: m's highest bit is set, or m = 0.
+struct Sum {
+    uint64_t m;
+    int n;
+};
+// The weight of a group whose first value weighs `first` (low in 2^-63), cut to 64 bits.
+W_FN Sum weight_of_group(uint64_t high, uint64_t low, Weight first) {
     const uint64_t m = mantissa(first);
-    const unsigned __int128 s = (unsigned __int128)high * m + (((unsigned __int128)low * m) >> 32);      // 2^(first.n - 79)
-    const int by = 17 - first.n + e;
-    return by < 128 ? (uint64_t)(s >> by) : 0;
+    const unsigned __int128 s = (unsigned __int128)high * m + (((unsigned __int128)low * m) >> 32);
+    const uint64_t h = (uint64_t)(s >> 64), l = (uint64_t)s;
+    if (!(h | l)) return {0, 0};
+#ifdef __CUDA_ARCH__
+    const int zeros = h ? __clzll((long long)h) : 64 + __clzll((long long)l);
+#else
+    const int zeros = h ? __builtin_clzll(h) : 64 + __builtin_clzll(l);
+#endif
+    return {(uint64_t)((s << zeros) >> 64), first.n - 79 + 64 - zeros};
+}
+// In units of 2^-10, more than it is by one at most; and the e with which sums whose numbers
+// of those add up to `total` stay below 2^62 units of 2^(e - 62): of 2^-59 of the whole (1 or
+// more, of 2048 sums at most) or less.
+W_FN uint32_t roughly(Sum s) {
+    const int by = -10 - s.n;
+    return (by < 64 ? (uint32_t)(s.m >> by) : 0u) + (s.m != 0);
+}
+W_FN int units_for(uint32_t total) {
+#ifdef __CUDA_ARCH__
+    return 32 - __clz((int)total) - 10;
+#else
+    return 32 - __builtin_clz(total) - 10;
+#endif
+}
+W_FN uint64_t in_units(Sum s, int e) {
+    const int by = e - 62 - s.n;
+    return by < 64 ? s.m >> by : 0;
 }
 
 // a += count w

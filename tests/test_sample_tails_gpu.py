@@ -80,6 +80,27 @@ def test_one_step_below_the_first(w4, V, at, T, first):
     _two_levels(w4, V, T, at, first)
 
 
+# weights of 2^-36.4 to 2^-42: of these a few numbers below 1 draw, each among thousands of words
+@pytest.mark.parametrize("T", [6.2e-4, 6.07e-4, 6e-4, 5.91e-4, 5.8e-4, 5.71e-4, 5.63e-4, 5.55e-4, 5.5e-4, 5.45e-4, 5.4e-4, 5.37e-4])
+@pytest.mark.parametrize("first", [20.484375, 20.0])
+def test_words_that_few_numbers_reach(w4, T, first):
+    for at in (0, 262144, 524271):
+        _two_levels(w4, 524272, T, at, first)
+
+
+@pytest.mark.parametrize("T", [0.3, 4e-3, 1.1e-3, 8e-4, 7.1e-4])
+@pytest.mark.parametrize("V,n", [(524272, 200000), (300001, 65536), (131072, 1000)])
+def test_many_first_words(w4, V, n, T):
+    x = torch.full((1, V), 20.484375 - 2.0 ** -6, dtype=torch.float16)
+    x[0, V - n:] = 20.484375
+    w = _step(T, 2.0 ** -6)
+    M = n + (V - n) * w
+    for tail in (1.0, float((V - n) * w / M)):
+        u = _numbers(tail, 64)
+        got = w4.sample(x.cuda().expand(len(u), -1), _f(u) / 2 ** 24, _f([T] * len(u)))
+        _check(got, [(lambda j: V - n + j, n, Decimal(1)), (lambda j: j, V - n, w)], u, M)
+
+
 @pytest.mark.parametrize("T", [0.02, 0.0301, 0.11])
 def test_three_levels(w4, T):
     # 5 words, 1000 of the same 32 values' group, and 260000 of another group
