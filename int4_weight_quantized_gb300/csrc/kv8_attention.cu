@@ -65,7 +65,7 @@ namespace {
 
 using namespace w4a8;
 
-constexpr int W = 8;                 // warps per CTA
+constexpr int W = kv8::kSplitWarps;  // warps per CTA
 constexpr int TILE = 32;             // tokens per unit of the split
 constexpr int MAXC = 152 * 2;        // CTAs at most
 constexpr int MAXW = MAXC * W;       // workers (warps) at most

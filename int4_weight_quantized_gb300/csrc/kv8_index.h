@@ -19,6 +19,7 @@
 namespace kv8 {
 
 constexpr int kBlockTokens = 16;     // tokens that share a scale
+constexpr int kSplitWarps = 8;       // workers of a CTA of the split decode kernel, which may have one part together
 
 // First code of token `tok` of a page's head, and the scale of its block
 // (64-bit: a cache of more than 2^31 codes is ordinary).

@@ -712,7 +712,7 @@ __global__ void __launch_bounds__(JW * 32) kv8_join_kernel(const JoinArgs a) {
             ml[k] = make_float2(-INFINITY, 0.0f);
             if (i >= n) continue;
             const bool own = i >= n_shared;
-            const size_t at = own ? (pair + (size_t)kv8::part_worker(named.x, parts, 8, i - n_shared)) * a.G + h : at_shared + (size_t)i * 128;
+            const size_t at = own ? (pair + (size_t)kv8::part_worker(named.x, parts, kv8::kSplitWarps, i - n_shared)) * a.G + h : at_shared + (size_t)i * 128;
             ml[k] = *reinterpret_cast<const float2 *>((own ? a.own_ml : a.ws_ml) + at * 2);
             const float *from = (own ? a.own_o : a.ws_o) + at * D + 4 * lane;
 #pragma unroll
