@@ -138,6 +138,7 @@ w4a8_status launch_kv8_decode(const uint16_t *q, const Kv8Cache &c, const int32_
 struct Kv8Own {
     const int32_t *cu, *shared;
     int n;
+    const uint64_t *begun;           // kBegun once the kernel before has what it waits for
 };
 size_t kv8_own_workspace_bytes(int B, int Hq, int Hkv, int D, int T, int maxp);
 w4a8_status launch_kv8_own(const uint16_t *q, const Kv8Cache &c, const int32_t *table, const int32_t *lens, const Kv8Own &own, int B, int Hq,

@@ -51,7 +51,9 @@ __device__ __forceinline__ int page_at(const int32_t *table, int b, int maxp, in
 namespace w4a8_host {
 
 // Launch as a programmatic dependent of the kernel before it on the stream:
-// the kernel begins with griddepcontrol.wait, so only its launch overlaps.
+// the kernel begins with griddepcontrol.wait, so only its launch overlaps.  (But for the
+// kernel of own tokens, kv8_decode_kernel<.., true>, which runs beside kv8_shared_kernel: it
+// acquires a word that the other releases behind its own wait, and waits at its end.)
 template <class... Params, class... Args>
 inline w4a8_status launch_dependent(void (*kern)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
                                     Args &&...args) {

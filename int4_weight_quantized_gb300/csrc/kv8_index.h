@@ -92,4 +92,7 @@ KV8_FN int part_worker(int first, Parts p, int W, int i) {
     return first + i + (W - 1) * groups;
 }
 
+// What the kernel of shared pages writes for the kernel of own tokens (kv8_shared.cu).
+constexpr uint64_t kBegun = 0x6b76385f62656775ull;
+
 }  // namespace kv8

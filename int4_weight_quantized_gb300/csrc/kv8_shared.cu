@@ -100,6 +100,7 @@ struct SharedArgs {
     const int32_t *table, *lens, *cu, *shared;
     float *ws_o, *ws_ml;             // parts: [tile + CTA][128][D], [..][128][2]
     Rec *ws_rec;                     // [B]
+    uint64_t *begun;                 // this kernel has waited for those before it
     int P, Hkv, T, T_log2, B, maxp, G, n;
     float scale_log2;
     int *status;
@@ -230,6 +231,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_shared_kernel(const SharedArgs
     }
     for (int g = threadIdx.x; g < a.n; g += THREADS) tab_tokens[g] = 0;
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    // (in front of launch_dependents, and behind the wait of this thread: the kernel of own
+    // tokens reads by this word alone what earlier kernels wrote)
+    if (blockIdx.x == 0 && threadIdx.x == 0) asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(a.begun), "l"(kv8::kBegun) : "memory");
     const int limit0 = (int)threadIdx.x < a.B ? row_limit(a, threadIdx.x) : 0;       // on its way with cu
     // Tensor memory is taken after the kernel before this one has ended and before the
     // next one may begin (two kernels on an SM that each hold some would wait for
@@ -315,6 +319,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv8_shared_kernel(const SharedArgs
     const int u0 = (int)kv8::first_unit(c, u_all, ctas), u1 = (int)kv8::first_unit(c + 1, u_all, ctas);
 
     tc_fence_after();
+    // (behind griddepcontrol.wait in every thread, and behind `begun`: own tokens start here)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint32_t tmem = *tslot;
     const Waiter wait = {abort_flag, a.budget, a.status};
@@ -670,6 +675,7 @@ struct JoinArgs {
     const Rec *rec;
     const float *own_o, *own_ml;     // own parts: [pair + worker][G][D], [..][G][2]
     const int2 *own_parts;           // [B][Hkv]
+    uint64_t *begun;
     uint16_t *out;
     int Hkv, G;
 };
@@ -682,6 +688,7 @@ __global__ void __launch_bounds__(JW * 32) kv8_join_kernel(const JoinArgs a) {
     __shared__ float2 sm_ml[JW * 32 / LW];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.begun = 0;        // for the workspace's next call
     const int hq = blockIdx.x, b = blockIdx.y, worker = threadIdx.x / LW, lane = threadIdx.x % LW, workers = blockDim.x / LW;
     const int head = hq / a.G, h = hq - head * a.G;
     const size_t pair = (size_t)b * a.Hkv + head;
@@ -783,8 +790,8 @@ struct Layout {
 Layout layout_of(int B, int n, int Hq, int Hkv, int D, int T, int maxp) {
     const size_t slots = (size_t)(most_tiles(B, n, Hq / Hkv, Hkv) + MAXC) * 128;
     Layout l;
-    l.o = 0;
-    l.ml = align256(slots * D * 4);
+    l.o = 256;                                                       // (behind `begun`)
+    l.ml = l.o + align256(slots * D * 4);
     l.rec = l.ml + align256(slots * 8);
     l.own = l.rec + align256((size_t)B * sizeof(Rec));
     l.bytes = l.own + w4a8_host::kv8_own_workspace_bytes(B, Hq, Hkv, D, T, maxp);
@@ -803,12 +810,13 @@ w4a8_status launch(const SharedArgs &s, const w4a8_host::Kv8Cache &c, const Layo
     st = w4a8_host::launch_dependent(kv8_shared_kernel<D>, dim3(grid), THREADS, (size_t)Cfg<D>::SMEM, stream, s);
     if (st != W4A8_OK) return st;
     JoinArgs j = {};
-    const w4a8_host::Kv8Own own = {s.cu, s.shared, s.n};
+    const w4a8_host::Kv8Own own = {s.cu, s.shared, s.n, s.begun};
     st = w4a8_host::launch_kv8_own(s.q, c, s.table, s.lens, own, s.B, Hq, s.maxp, scale, ws + l.own, &j.own_o, &j.own_ml, &j.own_parts, stream);
     if (st != W4A8_OK) return st;
     j.ws_o = s.ws_o;
     j.ws_ml = s.ws_ml;
     j.rec = s.ws_rec;
+    j.begun = s.begun;
     j.out = out;
     j.Hkv = s.Hkv;
     j.G = s.G;
@@ -835,7 +843,7 @@ size_t kv8_shared_workspace_bytes(int B, int n, int Hq, int Hkv, int D, int T, i
 w4a8_status launch_kv8_shared(const uint16_t *q, const Kv8Cache &c, const int32_t *table, const int32_t *lens, const int32_t *cu,
                               const int32_t *shared, int B, int n, int Hq, int maxp, float scale, uint16_t *out, void *workspace,
                               cudaStream_t stream) {
-    if (const int k = kv8_shared_pair_ctas(B, c.Hkv, c.T, maxp)) return launch_kv8_shared_pair(q, c, table, lens, {cu, shared, n}, B, Hq, maxp, scale, out, k, stream);
+    if (const int k = kv8_shared_pair_ctas(B, c.Hkv, c.T, maxp)) return launch_kv8_shared_pair(q, c, table, lens, {cu, shared, n, nullptr}, B, Hq, maxp, scale, out, k, stream);
     const Layout l = layout_of(B, n, Hq, c.Hkv, c.D, c.T, maxp);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     SharedArgs a = {};
@@ -848,6 +856,7 @@ w4a8_status launch_kv8_shared(const uint16_t *q, const Kv8Cache &c, const int32_
     a.lens = lens;
     a.cu = cu;
     a.shared = shared;
+    a.begun = reinterpret_cast<uint64_t *>(ws);
     a.ws_o = reinterpret_cast<float *>(ws + l.o);
     a.ws_ml = reinterpret_cast<float *>(ws + l.ml);
     a.ws_rec = reinterpret_cast<Rec *>(ws + l.rec);
