@@ -132,23 +132,32 @@ W_FN uint32_t fixed_next(Weight w) { return (uint32_t)cut(w, 74) & 2047u; }
 // off by 2^-55 together.
 W_FN bool is_steep(uint64_t last) { return last < (1ull << 41); }
 
-// A sum m 2^n: m's highest bit is set, or m = 0.
+#ifdef __CUDA_ARCH__
+W_FN int leading_zeros(uint64_t x) { return __clzll((long long)x); }
+W_FN uint64_t high_product(uint64_t a, uint64_t b) { return __umul64hi(a, b); }
+#else
+W_FN int leading_zeros(uint64_t x) { return x ? __builtin_clzll(x) : 64; }
+W_FN uint64_t high_product(uint64_t a, uint64_t b) { return (uint64_t)(((unsigned __int128)a * b) >> 64); }
+#endif
+
+// A sum m 2^n; m is 2^60 or more, or 0.
 struct Sum {
     uint64_t m;
     int n;
 };
-// The weight of a group whose first value weighs `first` (low in 2^-63), cut to 64 bits.
+// The weight of a group whose first value weighs `first` (low in 2^-63), cut to 60 bits.
 W_FN Sum weight_of_group(uint64_t high, uint64_t low, Weight first) {
-    const uint64_t m = mantissa(first);
-    const unsigned __int128 s = (unsigned __int128)high * m + (((unsigned __int128)low * m) >> 32);
-    const uint64_t h = (uint64_t)(s >> 64), l = (uint64_t)s;
-    if (!(h | l)) return {0, 0};
-#ifdef __CUDA_ARCH__
-    const int zeros = h ? __clzll((long long)h) : 64 + __clzll((long long)l);
-#else
-    const int zeros = h ? __builtin_clzll(h) : 64 + __builtin_clzll(l);
-#endif
-    return {(uint64_t)((s << zeros) >> 64), first.n - 79 + 64 - zeros};
+    if (!(high | low)) return {0, 0};
+    high += low >> 32;                           // (below 2^52)
+    if (!high) {
+        high = (uint32_t)low;
+        low = 0;
+        first.n -= 32;
+    }
+    const int zeros = leading_zeros(high);       // 12 to 63
+    // the sum's highest 64 bits, in 2^(-31 - zeros)
+    const uint64_t s = high << zeros | (uint64_t)(uint32_t)low << 32 >> (64 - zeros);
+    return {high_product(s, mantissa(first) << 14), first.n - zeros - 29};
 }
 // In units of 2^-10, more than it is by one at most; and the e with which sums whose numbers
 // of those add up to `total` stay below 2^62 units of 2^(e - 62): of 2^-59 of the whole (1 or
@@ -165,8 +174,8 @@ W_FN int units_for(uint32_t total) {
 #endif
 }
 W_FN uint64_t in_units(Sum s, int e) {
-    const int by = e - 62 - s.n;
-    return by < 64 ? s.m >> by : 0;
+    const int by = e - 62 - s.n;                 // -1 or more
+    return by < 0 ? s.m << -by : by < 64 ? s.m >> by : 0;
 }
 
 // a += count w

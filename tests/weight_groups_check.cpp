@@ -49,7 +49,7 @@ int main(int, char **argv) {
         }
         if (steep) low = ((low << 11) + next) >> 11;
         const weight::Sum s = weight::weight_of_group(high, low, weight::of(value(d0), top, c, weight::kPowers));
-        if (s.m && !(s.m >> 63)) return 1;
+        if (s.m && !(s.m >> 60)) return 1;
         const long double got = ldexpl((long double)s.m, s.n);
         // (of a steep group's steps 2^-74 is cut)
         const long double cut = steep ? words * ldexpl(expl(((long double)value(d0) - top) / (long double)T), -74) : 0;
