@@ -335,7 +335,8 @@ w4a8_status w4a8_decode_attention_kv8(const uint16_t *q, const w4a8_kv8 *cache, 
  *           min(lens[b], shared[b] page_tokens) are read from the pages that the
  *           first row's table entries name, the others from b's own entries.
  * Otherwise as above, with groups >= 0 and a workspace of
- * w4a8_decode_attention_kv8_shared_workspace_bytes (0 for an invalid shape).
+ * w4a8_decode_attention_kv8_shared_workspace_bytes (0 for an invalid shape; asked for
+ * also where tables are so short that one launch does all and leaves it alone).
  * W4A8_ERR_UNSUPPORTED for more than 1024 groups, and where (B Hq / 128 + groups
  * heads) max_pages page_tokens / 128 (64 at dimension 256) is not below 2^31.  Neither
  * out nor the workspace may overlap anything else. */
@@ -380,14 +381,16 @@ w4a8_status w4a8_kv8_compact(const w4a8_kv8 *cache, const int32_t *table, const 
  * it, its own included, are more than there are, where max_pages page_tokens
  * tokens are not enough for it, or where add[b] < 0.  Also written:
  *   start    [S]   the rows' lengths before, max_pages page_tokens where refused:
- *                  with these w4a8_kv8_append drops a refused row's tokens
+ *                  with these w4a8_kv8_append drops a refused row's tokens and sets the
+ *                  device status W4A8_ERR_PAGE, as for any token without a page: where rows
+ *                  are refused that status says no more than `refused` does
  *   cu       [S+1] where each row's new tokens are in the packing: sums of add (up to 2^31 - 1)
  *   slots    [total] page * page_tokens + token of each packed new token, -1 for
  *                  those of refused rows, on no page, and behind cu[S]
  *   refused  [1]   how many rows were refused
  * Needs a workspace of w4a8_kv8_extend_workspace_bytes (0 for an invalid shape, and for
- * small tables, which one launch takes); no two of the arrays may overlap; up to 12582912 pages whose tokens number less
- * than 2^31 (W4A8_ERR_UNSUPPORTED above). */
+ * small tables, which one launch takes); no two of the arrays may overlap; up to 12582912
+ * pages whose tokens number less than 2^31 (W4A8_ERR_UNSUPPORTED above). */
 size_t w4a8_kv8_extend_workspace_bytes(int pages, int S, int max_pages, int total);
 w4a8_status w4a8_kv8_extend(int32_t *table, int32_t *lens, const int32_t *add, int S, int max_pages, int page_tokens,
                             int pages, int total, int32_t *start, int32_t *cu, int32_t *slots, int32_t *refused,
@@ -404,12 +407,12 @@ w4a8_status w4a8_kv8_extend(int32_t *table, int32_t *lens, const int32_t *add, i
  * beginning passes u[b] M, logprobs[b] = ln(w_j / M).  Where T is not above 0 the
  * first word alone is kept.  NaN and -inf are never chosen; a row of nothing else
  * gets token -1 and logprob -inf.  Beside +inf everything else has weight 0.
- * A weight is computed to 2^-40 of itself, M and the sums from the beginning to 2^-39 of
- * themselves, and a row's results are the same in every batch.  The settings may be NULL (T = 1, no filter), as may
- * logprobs.  u, settings and results are [B], device, 4-byte aligned; logits are
- * 2-byte aligned.  Requires ld >= V, or ld = 0 (one row of
- * logits for all), 1 <= V <= 524272 (W4A8_ERR_UNSUPPORTED above);
- * B may be 0; the results may not overlap anything else.  Needs no workspace. */
+ * A weight is computed to 2^-40 of itself (2^-38 where it is below 2^-43), M and the sums
+ * from the beginning to 2^-39 of themselves, and a row's results are the same in every
+ * batch.  The settings may be NULL (T = 1, no filter), as may logprobs.  u, settings and
+ * results are [B], device, 4-byte aligned; logits are 2-byte aligned.  Requires ld >= V, or
+ * ld = 0 (one row of logits for all), 1 <= V <= 524272 (W4A8_ERR_UNSUPPORTED above); B may
+ * be 0; the results may not overlap anything else.  Needs no workspace. */
 w4a8_status w4a8_sample(const uint16_t *logits, long long ld, int B, int V, const float *u, const float *temperature,
                         const int32_t *top_k, const float *top_p, const float *min_p, int32_t *tokens, float *logprobs,
                         cudaStream_t stream);

@@ -29,7 +29,7 @@
 // one, to 2^-32 of that below), its sum is not.
 //
 // What bounds it.  64 sequences that share 8192 tokens and have 512 of their own, 32 heads
-// on 8 of 128 (84 MB of codes, 9 GFLOP): 43 us for all three, 23 of them 1. and about 13 2.
+// on 8 of 128 (84 MB of codes, 9 GFLOP): 44 us for all three, 23 of them 1. and about 13 2.
 // 256 that share 8192, 16 heads on 2 of 256 (74 MB, 35 GFLOP): 71 us, 40 of them 1.  One
 // row tile's step takes 2350 cycles (D = 256: 1770), 512 of them the products: a chain of
 // product, scores out of tensor memory, maximum, 2^x, weights back, product; the tensor
@@ -41,7 +41,8 @@
 // and two softmax groups with tiles in turn (44); weights beside the scores in one pass
 // (43, and 80 for the second case); own codes fetched to L2 beside the shared ones (47, 77:
 // they delay 1.'s copies, and 2. is bound by latency, not by the memory); fewer CTAs for few
-// steps, so that 2. runs beside them (25 -> 28 for the 7 groups, and slower for most sizes).
+// steps, so that 2. runs beside them (25 -> 28 for the 7 groups, and slower for most sizes, but 22 ->
+// 15 for 4 sequences of D = 256 in tables of 10240 tokens: a rule by D and tiles was not tried).
 #include <math.h>
 
 #include "attention.cuh"

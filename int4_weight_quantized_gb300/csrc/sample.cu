@@ -22,18 +22,20 @@
 // them into units of 2^-59 or less of their sum, and its first warp looks the borders up in
 // them; the CTA that has the word finds it.  (Rounded in each CTA, a group's sum would depend
 // on how the words are dealt out; with units of 2^-44 of the first word numbers next to 1 drew
-// a neighbour of the word that they stand for: 2^19 words of 2^-41 are 2^-22 of a row.  A share of the values for each CTA, summed over all CTAs' counts, was a
-// third of the time: shared memory of other CTAs is read at 10 bytes a cycle.)
+// a neighbour of the word that they stand for: 2^19 words of 2^-41 are 2^-22 of a row.  A
+// share of the values for each CTA, summed over all CTAs' counts, was a third of the time:
+// shared memory of other CTAs is read at 10 bytes a cycle.)
 //
 // What bounds it: a CTA's chain of phases, one CTA to an SM.  256 rows of 262144 words, 4
-// CTAs to a row, take 172 us, 36 rows at once (the words alone, 134 MB, 20): clearing the
-// counts 1 us, the words' way here 3, counting 65536 words 5.5 (a warp's addition to shared
-// memory takes 4.9 cycles), weights 4.5, looking the borders up 2 and 1 to 1.5 a filter (min-p beside the others),
-// finding the word 0.5 to 2, three barriers of the cluster 0.8 each.  64 rows of 131072, 2 CTAs each:
-// 22.5 us; one of 32000, 8 CTAs: 13.5.  More CTAs to a row than its words need are
-// taken while all rows' are resident together: 8 for one row of 32000 words 13.5 us where
-// one would count 32000 words alone.  The words stay in registers: read again for the last
-// phase, 256 rows took 185 us instead of 169.
+// CTAs to a row, take 171 us, 36 rows at once (the words alone, 134 MB, 20): clearing the
+// counts 1 us, the words' way here and counting 65536 of them 7 (a warp's addition to shared
+// memory takes 4.9 cycles), weights 3.5, their units 1.9, looking the borders up 2 and 1 to 1.5
+// a filter (min-p beside the others), finding the word 0.5 to 2, three barriers of the cluster
+// 0.8 each.  64 rows of 131072, 2 CTAs each: 22.4 us; one of 32000, 8 CTAs: 13.4.  More CTAs to
+// a row than its words need are taken while all rows' are resident together: 8 for one row of
+// 32000 words 13.4 us where one would count 32000 words alone.  The words stay in registers:
+// read again for the last phase, 256 rows took 185 us instead of 169.  (With sums rounded in
+// every CTA, which were less exact, 163, 21.4 and 13.4.)
 #include <math.h>
 
 #include "common.cuh"
